@@ -2,7 +2,8 @@
  * ds_topk.h -- C ABI of libdstopk.so, the selection step of DeepSeek-style
  * sparse attention on B200 (sm_100a).
  *
- * Five operations, as described on the pages this library follows:
+ * Five operations, as described on the pages this library follows, and an
+ * 8-bit form of the cache that the last of them reads:
  *
  *  - Row-wise top-k of given scores (DeepSelect hub page, use-case paragraphs:
  *    pick the top-k positions of every score row; bfloat16 rows for the
@@ -61,8 +62,13 @@
 extern "C" {
 #endif
 
-/* element types of score rows */
-typedef enum { DS_F32 = 0, DS_BF16 = 1 } ds_dtype;
+/* element types of score rows (the first two) and of cached rows */
+typedef enum {
+  DS_F32 = 0,
+  DS_BF16 = 1,
+  DS_E4M3 = 2, /* cached rows: 8-bit floating point, 4 exponent and 3 mantissa bits, largest 448 */
+  DS_I8 = 3    /* cached rows: signed 8-bit integers, written as -127..127 */
+} ds_dtype;
 
 /* status codes */
 #define DS_OK 0
@@ -81,6 +87,8 @@ typedef enum { DS_F32 = 0, DS_BF16 = 1 } ds_dtype;
 #define DS_ATTN_MAX_DIM 512      /* largest head_dim of ds_sparse_attention */
 #define DS_ATTN_MAX_WINDOW 4096  /* largest sliding window of ds_sparse_attention */
 #define DS_ATTN_MAX_HEADS 4096   /* largest number of query heads of ds_sparse_attention */
+#define DS_CACHE_MAX_BLOCK 128   /* largest block of rows that shares one scale */
+#define DS_CACHE_MAX_ARRAYS 8    /* arrays that one ds_cache_compact call moves */
 
 /*
  * ds_topk -- top-k of every row of a [batch, n] score matrix.
@@ -322,6 +330,173 @@ int ds_sparse_attention(const void* q, const void* kv, int64_t kv_batch_stride, 
                         const int32_t* idx, int k, const void* win, int W, const int32_t* win_len,
                         const float* sink, int batch, int heads, int d, float scale,
                         void* out, float* lse, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A cache in 8 bits that stays bounded: ds_cache_quantize writes rows into it,
+ * ds_sparse_attention_q8 attends over it, ds_attention_mass accounts for the
+ * weight each row received, ds_cache_evict picks what stays and
+ * ds_cache_compact moves it.  (The pages keep the compressed cache in 16 bits
+ * and never shorten it: these five are an extension of the attention above,
+ * with its conventions.)
+ *
+ * The cache of one batch row is T rows of kv_heads x d codes, [T, kv_heads, d],
+ * with one float32 scale for each block of `block` rows and each KV head,
+ * [ceil(T / block), kv_heads]: row r of KV head g stands for
+ *     scale[r / block, g] * code[r, g, :].
+ * block is 1, 2, 4 .. DS_CACHE_MAX_BLOCK; d a multiple of 64, 64 ..
+ * DS_ATTN_MAX_DIM; kv_heads >= 1; codes are DS_E4M3 or DS_I8, 16-byte aligned.
+ *
+ * None of the five allocates memory, keeps state between calls or uses the
+ * scratch buffers: calls on different streams may overlap, and all may be
+ * captured into CUDA graphs after a first call on the device.
+ */
+
+/*
+ * ds_cache_quantize -- write bfloat16 rows into an 8-bit cache.
+ *
+ * For the rows of the call that fall into one block, and each KV head, with
+ * a = max(max |x|, 2^-100) and M = 448 (DS_E4M3) or 127 (DS_I8):
+ *     scale = a / M;   code = x * (M / a) rounded to nearest even
+ * with the quotients and the product in float32.  If a value of the block is
+ * not finite, its scale is NaN and its codes 0 (the block reads as NaN).
+ *
+ * rows     device bfloat16: row r of batch row b is the kv_heads * d elements
+ *          at rows + b * rows_batch_stride + r * row_stride; 16-byte aligned,
+ *          both strides in elements, multiples of 8; row_stride >= kv_heads * d,
+ *          rows_batch_stride >= 0.
+ * batch    1 .. 65535;  n >= 1 rows given for every batch row;
+ *          batch * kv_heads * ceil(n / block) <= 2147483647.
+ * pos      device int32 [batch] or NULL (= 0): the cache row that the first row
+ *          goes to, a multiple of block in [0, T] (a block is written whole, so
+ *          that its scale covers it: rows of an unfinished block wait in the
+ *          attention's window).  A batch row with any other pos is left as it
+ *          was (libdstopk_debug.so records DS_ERR_RANGE).
+ * len      device int32 [batch] or NULL (= n): the first
+ *          min(max(len[b], 0), n, T - pos[b]) rows are written; everything else
+ *          in codes and scales is left as it was.  A last block that is not
+ *          full has the scale of the rows given.
+ * codes    device: batch row b's cache starts codes_batch_stride * b rows after
+ *          codes; >= T if batch > 1.
+ * scales   device float32: batch row b's scales start scales_batch_stride * b
+ *          blocks (of kv_heads scales) after scales; >= ceil(T / block) if
+ *          batch > 1.
+ * Returns DS_OK, DS_ERR_ARG, DS_ERR_UNSUPPORTED or DS_ERR_CUDA.
+ */
+int ds_cache_quantize(const void* rows, int64_t rows_batch_stride, int64_t row_stride, int batch, int n, int kv_heads,
+                      int d, int dtype, int block, const int32_t* pos, const int32_t* len, void* codes,
+                      int64_t codes_batch_stride, float* scales, int64_t scales_batch_stride, int T, void* stream);
+
+/*
+ * ds_sparse_attention_q8 -- ds_sparse_attention over an 8-bit cache.
+ *
+ * The formula, the slots, the window, the sink and the empty case are those of
+ * ds_sparse_attention, with KV heads: query head h reads KV head
+ * h / (heads / kv_heads) of every attended row, and every KV head attends over
+ * the same slots.
+ *
+ * q, idx, k, win_len, sink, batch, heads, scale, out, lse  as there.
+ * codes, scales  the cache; codes_batch_stride (rows) and scales_batch_stride
+ *          (blocks) >= 0 lead from one batch row's cache to the next: 0 and 0
+ *          for one cache shared by every batch row.
+ * dtype    DS_E4M3 or DS_I8;  T >= 1 rows of each cache.
+ * win      device bfloat16 [batch, W, kv_heads, d] or NULL (then W must be 0);
+ *          16-byte aligned; 0 <= W <= DS_ATTN_MAX_WINDOW.
+ * kv_heads divides heads.
+ * Scales and window rows are expected to be finite; what is attended and not
+ * finite makes the outputs of its KV head's query heads NaN.  Rows and scales
+ * that no slot names are not read.
+ * Returns DS_OK, DS_ERR_ARG, DS_ERR_UNSUPPORTED or DS_ERR_CUDA.
+ */
+int ds_sparse_attention_q8(const void* q, const void* codes, int64_t codes_batch_stride, const float* scales,
+                           int64_t scales_batch_stride, int dtype, int block, int T, const int32_t* idx, int k,
+                           const void* win, int W, const int32_t* win_len, const float* sink, int batch, int heads,
+                           int kv_heads, int d, float scale, void* out, float* lse, void* stream);
+
+/*
+ * ds_attention_mass -- add the attention weight that every selected row
+ * received, summed over the query heads, to the row's account:
+ *     mass[b, idx[b, j]] += sum_h exp(scale * (q[b, h, :] . row) - lse[b, h])
+ * for the slots j with 0 <= idx[b, j] < T.  With the lse of ds_sparse_attention
+ * or ds_sparse_attention_q8 on the same inputs these are the softmax's weights
+ * (a window's and the sink's shares are in lse and go to no account).
+ *
+ * cache    the 8-bit cache (dtype DS_E4M3 or DS_I8, with scales and block), or
+ *          the bfloat16 cache [T, kv_heads, d] of every batch row (dtype
+ *          DS_BF16; scales NULL, block and scales_batch_stride ignored);
+ *          cache_batch_stride in rows, >= 0.
+ * lse      device float32 [batch, heads]; heads whose lse is -inf add nothing.
+ * mass     device float32: batch row b's account is the T values that start
+ *          mass_batch_stride * b after mass; >= T if batch > 1, so that no two
+ *          batch rows share an account.
+ * The other arguments are those of ds_sparse_attention_q8; k = 0 adds nothing.
+ * Each slot's weight is summed over the heads in a fixed order and added once.
+ * A row named by several slots of a batch row gets one addition for each, in an
+ * order that may differ from call to call (the sum of three or more such
+ * additions may differ in its last bits); with distinct slots, as ds_topk gives
+ * them, results do not vary.
+ * Returns DS_OK, DS_ERR_ARG, DS_ERR_UNSUPPORTED or DS_ERR_CUDA.
+ */
+int ds_attention_mass(const void* q, const void* cache, int64_t cache_batch_stride, const float* scales,
+                      int64_t scales_batch_stride, int dtype, int block, int T, const int32_t* idx, int k,
+                      const float* lse, int batch, int heads, int kv_heads, int d, float scale, float* mass,
+                      int64_t mass_batch_stride, void* stream);
+
+/*
+ * ds_cache_evict -- which blocks of each batch row's cache stay.
+ *
+ * Batch row b holds L = min(max(len[b], 0), T) rows in ceil(L / block) blocks,
+ * the last of them perhaps not full.  A block's key is the sum of its rows'
+ * accounts, in float64, rounded once to float32.  At most `budget` blocks stay:
+ * the first keep_first and the last keep_last, then those with the largest
+ * keys; equal keys go to the lower block, -0.0 equals +0.0, a NaN ranks above
+ * +inf.  (A block, not a row, is what leaves: its rows share a scale.)
+ *
+ * mass     device float32, batch row b's account mass_batch_stride * b values
+ *          after mass (>= 0).
+ * T        1 .. 16777216;  len  device int32 [batch] or NULL (= T).
+ * budget   1 .. ceil(T / block);  keep_first, keep_last >= 0, together at most
+ *          budget.
+ * kept     device int32 [batch, budget]: the blocks that stay, ascending, then
+ *          -1 where fewer than budget blocks are held.
+ * new_len  device int32 [batch]: the rows in them; may be len itself only if
+ *          no later call needs the old lengths (ds_cache_compact does).
+ * Returns DS_OK, DS_ERR_ARG, DS_ERR_UNSUPPORTED or DS_ERR_CUDA.
+ */
+int ds_cache_evict(const float* mass, int64_t mass_batch_stride, int batch, int T, const int32_t* len, int block,
+                   int budget, int keep_first, int keep_last, int32_t* kept, int32_t* new_len, void* stream);
+
+/* One array that ds_cache_compact moves: batch row b's items, item_bytes each
+ * and one after the other, start b * src_batch_stride bytes after src, and go
+ * to dst likewise.  per_block 0: an item for each row (codes, keys, accounts);
+ * 1: an item for each block (scales). */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t src_batch_stride;
+  int64_t dst_batch_stride;
+  int64_t item_bytes; /* 1 .. 16777216 */
+  int per_block;
+} ds_cache_array;
+
+/*
+ * ds_cache_compact -- move the blocks of a list to the front of other buffers.
+ *
+ * For every array (host memory, read before the call returns), batch row b and
+ * entry j with 0 <= kept[b, j] < ceil(L / block): block kept[b, j] of src goes
+ * to block j of dst, as far as its rows are below L = min(max(len[b], 0), T).
+ * Nothing else of dst is written.
+ *
+ * n_arrays 1 .. DS_CACHE_MAX_ARRAYS.
+ * kept     device int32 [batch, budget], for instance ds_cache_evict's; budget
+ *          1 .. ceil(T / block).  len  the lengths before the eviction, device
+ *          int32 [batch] or NULL (= T); T 1 .. 16777216 rows of every src.
+ * Batch strides, if batch > 1, are at least the bytes of a batch row: src T
+ * items (ceil(T / block) with per_block), dst min(T, budget * block) (budget).
+ * src and dst of an array must not overlap (DS_ERR_ARG).
+ * Returns DS_OK, DS_ERR_ARG, DS_ERR_UNSUPPORTED or DS_ERR_CUDA.
+ */
+int ds_cache_compact(const ds_cache_array* arrays, int n_arrays, const int32_t* kept, int budget, const int32_t* len,
+                     int batch, int T, int block, void* stream);
 
 /*
  * ds_get_device_status -- synchronise `stream`, then return and clear the

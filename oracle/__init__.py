@@ -32,6 +32,9 @@ selection step computes, in float64:
                     request, steps table row 1).  PARITY UNPINNED: the pages do
                     not give the gate, so the function follows a stated reading.
 
+* ``cache``      -- the 8-bit cache: quantised rows, the attention over them, the
+                    account of the attention received, eviction and compaction.
+
 Every function is pinned by the ``-m "not gpu"`` tests in ``tests/test_oracle_*``
 against brute force, closed forms, hand-worked examples under ``tests/golden``
 and invariants.  ``compress_fold`` alone is "parity unpinned": its pins check
@@ -44,8 +47,9 @@ from .indexer import indexer_scores, indexer_topk
 from .attention import sparse_attention
 from .qproj import qproj, round_bf16
 from .compress import compress_fold
+from . import cache
 
 __all__ = [
     "decode_bf16", "decode_f32", "NEG_INF_BF16", "NEG_INF_F32",
-    "topk_rows", "topk_row", "indexer_scores", "indexer_topk", "sparse_attention", "qproj", "round_bf16", "compress_fold",
+    "topk_rows", "topk_row", "indexer_scores", "indexer_topk", "sparse_attention", "qproj", "round_bf16", "compress_fold", "cache",
 ]

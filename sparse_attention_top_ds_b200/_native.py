@@ -6,6 +6,7 @@ fallback implementation.
 """
 
 import ctypes
+import math
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -15,6 +16,8 @@ DEBUG_LIB_PATH = os.path.join(_PKG, "libdstopk_debug.so")
 
 DS_F32 = 0
 DS_BF16 = 1
+DS_E4M3 = 2
+DS_I8 = 3
 
 DS_OK = 0
 DS_ERR_ARG = -1
@@ -30,8 +33,16 @@ DS_INDEXER_MAX_HEADS = 64
 DS_ATTN_MAX_DIM = 512
 DS_ATTN_MAX_WINDOW = 4096
 DS_ATTN_MAX_HEADS = 4096
+DS_CACHE_MAX_BLOCK = 128
+DS_CACHE_MAX_ARRAYS = 8
 
 _lib = None
+
+
+class _CacheArray(ctypes.Structure):
+    """ds_cache_array of the header."""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("src_batch_stride", ctypes.c_int64),
+                ("dst_batch_stride", ctypes.c_int64), ("item_bytes", ctypes.c_int64), ("per_block", ctypes.c_int)]
 
 
 class DsError(RuntimeError):
@@ -88,6 +99,19 @@ def load():
     lib.ds_debug_stash_stamps.restype = i32
     lib.ds_read_floor.argtypes = [vp, ctypes.c_int64, i32, vp]
     lib.ds_read_floor.restype = i32
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    lib.ds_cache_quantize.argtypes = [vp, i64, i64, i32, i32, i32, i32, i32, i32, i32p, i32p, vp, i64, vp, i64, i32, vp]
+    lib.ds_cache_quantize.restype = i32
+    lib.ds_sparse_attention_q8.argtypes = [vp, vp, i64, vp, i64, i32, i32, i32, i32p, i32, vp, i32, i32p, vp,
+                                           i32, i32, i32, i32, f32, vp, vp, vp]
+    lib.ds_sparse_attention_q8.restype = i32
+    lib.ds_attention_mass.argtypes = [vp, vp, i64, vp, i64, i32, i32, i32, i32p, i32, vp, i32, i32, i32, i32, f32,
+                                      vp, i64, vp]
+    lib.ds_attention_mass.restype = i32
+    lib.ds_cache_evict.argtypes = [vp, i64, i32, i32, i32p, i32, i32, i32, i32, i32p, i32p, vp]
+    lib.ds_cache_evict.restype = i32
+    lib.ds_cache_compact.argtypes = [ctypes.POINTER(_CacheArray), i32, i32p, i32, i32p, i32, i32, i32, vp]
+    lib.ds_cache_compact.restype = i32
     _lib = lib
     return lib
 
@@ -451,3 +475,322 @@ def ds_compress_fold(rows, gate, out=None, stream=None):
                                      _stream_ptr(stream))
     _check(rc, "ds_compress_fold")
     return out
+
+
+# ------------------------------------------------------------------ the 8-bit cache
+#
+# These calls run on ``stream`` (default: the tensors' device's current stream).
+# Given another stream, what they return is allocated on it, and every tensor is
+# recorded there, so that freeing a tensor does not hand out its memory early;
+# the caller orders the two streams, as for any other work.
+
+class _Call:
+    """Where a call runs: the tensors' device, and the stream."""
+
+    __slots__ = ("dev", "stream", "other", "tensors")
+
+    def __init__(self, dev, stream):
+        import torch
+        cur = torch.cuda.current_stream(dev)
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, expected {dev}")
+        self.dev = dev
+        self.stream = cur if stream is None else stream
+        self.other = cur if stream is not None and stream != cur else None
+        self.tensors = []
+
+    def need(self, t, dtype, name, shape=None, optional=False):
+        """Check an argument; shape entries of None match anything."""
+        import torch
+        if t is None and optional:
+            return None
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.device != self.dev:
+            raise ValueError(f"{name} is on {t.device}, expected {self.dev}")
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if shape is not None and (t.dim() != len(shape) or any(e is not None and e != n for e, n in zip(shape, t.shape))):
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        if self.other is not None:
+            self.tensors.append(t)
+        return t
+
+    def empty(self, shape, dtype):
+        import torch
+        if self.other is None:
+            return torch.empty(shape, dtype=dtype, device=self.dev)
+        with torch.cuda.stream(self.stream):
+            t = torch.empty(shape, dtype=dtype, device=self.dev)
+        t.record_stream(self.other)
+        return t
+
+    def run(self, where, fn, *args):
+        import torch
+        if torch.cuda.current_device() == self.dev.index:
+            rc = fn(*args, self.stream.cuda_stream)
+        else:
+            with torch.cuda.device(self.dev):
+                rc = fn(*args, self.stream.cuda_stream)
+        for t in self.tensors:
+            t.record_stream(self.stream)
+        _check(rc, where)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _cuda_device(t, name):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    return t.device
+
+
+def _dense(t, name, lead=1):
+    """t is contiguous behind its first ``lead`` dimensions (sizes of one have no stride)."""
+    step = 1
+    for n, st in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
+        if n != 1 and st != step:
+            raise ValueError(f"{name} must be contiguous behind dimension {lead}")
+        step *= n
+    return t
+
+
+def _steps(t, unit, name):
+    """Batch stride of t [batch, ...] in units of ``unit`` elements."""
+    if t.shape[0] == 1:
+        return t[0].numel() // unit
+    if t.stride(0) % unit:
+        raise ValueError(f"{name}: the batch stride must be whole rows")
+    return t.stride(0) // unit
+
+
+def _cache8_dtype(t, name):
+    import torch
+    if t.dtype == torch.float8_e4m3fn:
+        return DS_E4M3
+    if t.dtype == torch.int8:
+        return DS_I8
+    raise TypeError(f"{name} must be torch.float8_e4m3fn or torch.int8, got {t.dtype}")
+
+
+def _cache8(call, codes, scales, block, batch):
+    """(dtype, T, kv_heads, d, code rows, scale blocks from one batch row to the next)."""
+    call.need(codes, None, "codes")
+    dt = _cache8_dtype(codes, "codes")
+    if not isinstance(block, int) or block < 1:
+        raise ValueError("block must be a positive int")
+    if codes.dim() not in (3, 4) or (codes.dim() == 4 and codes.shape[0] != batch):
+        raise ValueError("codes must be [T, kv_heads, d] or [batch, T, kv_heads, d]")
+    T, kv_heads, d = codes.shape[-3:]
+    nb, f32 = (T + block - 1) // block, _torch().float32
+    if codes.dim() == 3:
+        call.need(scales, f32, "scales", (nb, kv_heads))
+        _dense(codes, "codes", 0), _dense(scales, "scales", 0)
+        strides = 0, 0
+    else:
+        call.need(scales, f32, "scales", (batch, nb, kv_heads))
+        _dense(codes, "codes"), _dense(scales, "scales")
+        strides = _steps(codes, max(1, kv_heads * d), "codes"), _steps(scales, max(1, kv_heads), "scales")
+    return (dt, T, kv_heads, d) + strides
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def ds_cache_quantize(rows, codes, scales, block, pos=None, length=None, stream=None):
+    """Write bfloat16 rows into an 8-bit cache, in place.
+
+    rows    bf16 [batch, n, kv_heads, d] (any batch and row strides);
+    codes   float8_e4m3fn or int8 [batch, T, kv_heads, d];
+    scales  float32 [batch, ceil(T / block), kv_heads];
+    block   rows that share a scale: 1, 2, 4 .. 128;
+    pos     int32 [batch] or None (= 0): where the first row goes, a multiple of block;
+    length  int32 [batch] or None (= n): how many rows are written.
+    Returns (codes, scales).
+    """
+    torch = _torch()
+    call = _Call(_cuda_device(rows, "rows"), stream)
+    call.need(rows, torch.bfloat16, "rows", (None, None, None, None))
+    batch, n, kv_heads, d = rows.shape
+    dt, T, ch, cd, cstep, sstep = _cache8(call, codes, scales, block, batch)
+    if codes.dim() != 4 or (ch, cd) != (kv_heads, d):
+        raise ValueError("codes must be [batch, T, kv_heads, d] with the rows' kv_heads and d")
+    _dense(rows, "rows", 2)
+    call.need(pos, torch.int32, "pos", (batch,), optional=True)
+    call.need(length, torch.int32, "length", (batch,), optional=True)
+    for t, name in ((pos, "pos"), (length, "length")):
+        if t is not None:
+            _dense(t, name, 0)
+    call.run("ds_cache_quantize", load().ds_cache_quantize, _at(rows), rows.stride(0) if batch > 1 else 0,
+             rows.stride(1) if n > 1 else kv_heads * d, batch, n, kv_heads, d, dt, block, _at(pos), _at(length),
+             _at(codes), cstep, _at(scales), sstep, T)
+    return codes, scales
+
+
+def ds_sparse_attention_q8(q, codes, scales, idx, block, scale=None, win=None, win_len=None, sink=None,
+                           return_lse=False, out=None, lse=None, stream=None):
+    """ds_sparse_attention over an 8-bit cache with KV heads.
+
+    q      bf16 [batch, heads, d];
+    codes  float8_e4m3fn or int8 [T, kv_heads, d] (one cache for every batch row)
+           or [batch, T, kv_heads, d];
+    scales float32 [ceil(T / block), kv_heads], with the batch in front as in codes;
+    idx    int32 [batch, k] or None (window only);  block  rows that share a scale;
+    win    bf16 [batch, W, kv_heads, d] or None;  win_len  int32 [batch] or None (= W);
+    sink   float32 [heads] or None;  scale  default 1/sqrt(d).
+    Query head h reads KV head h // (heads // kv_heads).
+    Returns out bf16 [batch, heads, d], or (out, lse float32 [batch, heads]).
+    """
+    torch = _torch()
+    call = _Call(_cuda_device(q, "q"), stream)
+    call.need(q, torch.bfloat16, "q", (None, None, None))
+    batch, heads, d = q.shape
+    dt, T, kv_heads, cd, cstep, sstep = _cache8(call, codes, scales, block, batch)
+    if cd != d:
+        raise ValueError("codes and q differ in d")
+    call.need(idx, torch.int32, "idx", (batch, None), optional=True)
+    call.need(win, torch.bfloat16, "win", (batch, None, kv_heads, d), optional=True)
+    call.need(win_len, torch.int32, "win_len", (batch,), optional=True)
+    call.need(sink, torch.float32, "sink", (heads,), optional=True)
+    k, W = 0 if idx is None else idx.shape[1], 0 if win is None else win.shape[1]
+    if out is None:
+        out = call.empty((batch, heads, d), torch.bfloat16)
+    else:
+        call.need(out, torch.bfloat16, "out", (batch, heads, d))
+    if lse is not None:
+        call.need(lse, torch.float32, "lse", (batch, heads))
+    elif return_lse:
+        lse = call.empty((batch, heads), torch.float32)
+    for t, name in ((q, "q"), (idx, "idx"), (win, "win"), (win_len, "win_len"), (sink, "sink"), (out, "out"), (lse, "lse")):
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    call.run("ds_sparse_attention_q8", load().ds_sparse_attention_q8, _at(q), _at(codes), cstep, _at(scales), sstep, dt,
+             block, T, _at(idx) if k else None, k, _at(win) if W else None, W, _at(win_len), _at(sink), batch, heads,
+             kv_heads, d, 1.0 / math.sqrt(d) if scale is None else float(scale), _at(out), _at(lse))
+    return (out, lse) if return_lse else out
+
+
+def ds_attention_mass(q, cache, idx, lse, mass, scales=None, block=1, scale=None, stream=None):
+    """Add the attention weight that every selected row received, summed over
+    the query heads, to the rows' accounts, in place.
+
+    q      bf16 [batch, heads, d];  idx  int32 [batch, k];
+    cache  an 8-bit cache as in ds_sparse_attention_q8, with its scales and block; or
+           a bf16 cache [T, d], [batch, T, d] or [batch, T, kv_heads, d], scales None;
+    lse    float32 [batch, heads] of the attention;  scale  default 1/sqrt(d);
+    mass   float32 [batch, T], rows contiguous.
+    Returns mass.
+    """
+    torch = _torch()
+    call = _Call(_cuda_device(q, "q"), stream)
+    call.need(q, torch.bfloat16, "q", (None, None, None))
+    batch, heads, d = q.shape
+    if scales is not None:
+        dt, T, kv_heads, cd, cstep, sstep = _cache8(call, cache, scales, block, batch)
+    else:
+        call.need(cache, torch.bfloat16, "cache")
+        if cache.dim() not in (2, 3, 4) or (cache.dim() > 2 and cache.shape[0] != batch):
+            raise ValueError("a bf16 cache must be [T, d], [batch, T, d] or [batch, T, kv_heads, d]")
+        T, kv_heads = (cache.shape[1], cache.shape[2]) if cache.dim() == 4 else (cache.shape[-2], 1)
+        dt, cd, sstep, block = DS_BF16, cache.shape[-1], 0, 1
+        _dense(cache, "cache", 0 if cache.dim() == 2 else 1)
+        cstep = 0 if cache.dim() == 2 else _steps(cache, max(1, kv_heads * cd), "cache")
+    if cd != d:
+        raise ValueError("cache and q differ in d")
+    call.need(idx, torch.int32, "idx", (batch, None))
+    call.need(lse, torch.float32, "lse", (batch, heads))
+    call.need(mass, torch.float32, "mass", (batch, T))
+    for t, name in ((q, "q"), (idx, "idx"), (lse, "lse")):
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    _dense(mass, "mass")
+    k = idx.shape[1]
+    call.run("ds_attention_mass", load().ds_attention_mass, _at(q), _at(cache), cstep, _at(scales), sstep, dt, block, T,
+             _at(idx) if k else None, k, _at(lse), batch, heads, kv_heads, d,
+             1.0 / math.sqrt(d) if scale is None else float(scale), _at(mass), _steps(mass, 1, "mass"))
+    return mass
+
+
+def ds_cache_evict(mass, budget, block=1, length=None, keep_first=0, keep_last=1, kept=None, new_length=None,
+                   stream=None):
+    """Which blocks of each batch row's cache stay, by accumulated attention weight.
+
+    mass    float32 [batch, T], rows contiguous;  length  int32 [batch] or None (= T);
+    budget  blocks that stay at most: the first ``keep_first`` and the last
+            ``keep_last``, then those whose rows' weights sum to the most.
+    Returns (kept int32 [batch, budget]: the blocks that stay, ascending, then -1;
+    new_length int32 [batch]: the rows in them).
+    """
+    torch = _torch()
+    call = _Call(_cuda_device(mass, "mass"), stream)
+    call.need(mass, torch.float32, "mass", (None, None))
+    batch, T = mass.shape
+    _dense(mass, "mass")
+    call.need(length, torch.int32, "length", (batch,), optional=True)
+    if not isinstance(budget, int) or not isinstance(block, int) or budget < 1:
+        raise ValueError("budget and block must be positive ints")
+    kept = call.empty((batch, budget), torch.int32) if kept is None else call.need(kept, torch.int32, "kept", (batch, budget))
+    if new_length is None:
+        new_length = call.empty((batch,), torch.int32)
+    else:
+        call.need(new_length, torch.int32, "new_length", (batch,))
+    for t, name in ((length, "length"), (kept, "kept"), (new_length, "new_length")):
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    call.run("ds_cache_evict", load().ds_cache_evict, _at(mass), _steps(mass, 1, "mass"), batch, T, _at(length), block,
+             budget, int(keep_first), int(keep_last), _at(kept), _at(new_length))
+    return kept, new_length
+
+
+def ds_cache_compact(kept, block=1, length=None, rows=(), blocks=(), stream=None):
+    """Move the blocks of a list (ds_cache_evict's) to the front of other buffers.
+
+    kept    int32 [batch, budget];  length  int32 [batch] or None: the lengths
+            before the eviction;
+    rows    pairs (src, dst) of arrays with one entry for each row, [batch, T, ...]
+            and [batch, at least min(T, budget * block), ...] (codes, keys, accounts);
+    blocks  pairs with one entry for each block, [batch, ceil(T / block), ...] and
+            [batch, at least budget, ...] (scales).
+    The arrays are contiguous behind the batch; a pair has one dtype and trailing
+    shape, and its buffers do not overlap.  Rows of dst behind what stays are left
+    as they were.
+    """
+    torch = _torch()
+    call = _Call(_cuda_device(kept, "kept"), stream)
+    call.need(kept, torch.int32, "kept", (None, None))
+    batch, budget = kept.shape
+    call.need(length, torch.int32, "length", (batch,), optional=True)
+    for t, name in ((kept, "kept"), (length, "length")):
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if not isinstance(block, int) or block < 1:
+        raise ValueError("block must be a positive int")
+    pairs = [(s, d, 0) for s, d in rows] + [(s, d, 1) for s, d in blocks]
+    if not 1 <= len(pairs) <= DS_CACHE_MAX_ARRAYS:
+        raise ValueError(f"1 to {DS_CACHE_MAX_ARRAYS} arrays can be moved")
+    call.need(pairs[0][0], None, "src")
+    T = pairs[0][0].shape[1] * (block if pairs[0][2] else 1) if pairs[0][0].dim() > 1 else 0
+    nb = (T + block - 1) // block
+    arrays = (_CacheArray * len(pairs))()
+    for a, (src, dst, per_block) in zip(arrays, pairs):
+        call.need(src, None, "src")
+        call.need(dst, src.dtype, "dst")
+        if src.dim() < 2 or src.shape[0] != batch or src.shape[1] != (nb if per_block else T):
+            raise ValueError(f"src must be [{batch}, {nb if per_block else T}, ...], got {list(src.shape)}")
+        least = budget if per_block else min(T, budget * block)
+        if dst.dim() != src.dim() or dst.shape[0] != batch or dst.shape[1] < least or dst.shape[2:] != src.shape[2:]:
+            raise ValueError(f"dst must be [{batch}, at least {least}, ...] like src, got {list(dst.shape)}")
+        _dense(src, "src"), _dense(dst, "dst")
+        size = src.element_size()
+        a.src, a.dst, a.per_block = src.data_ptr(), dst.data_ptr(), per_block
+        a.item_bytes = math.prod(src.shape[2:]) * size
+        a.src_batch_stride, a.dst_batch_stride = (src.stride(0) * size, dst.stride(0) * size) if batch > 1 else (0, 0)
+    call.run("ds_cache_compact", load().ds_cache_compact, arrays, len(pairs), _at(kept), budget, _at(length), batch, T,
+             block)

@@ -1,0 +1,247 @@
+// cache_ops.cuh -- the C ABI of the 8-bit cache: argument checks, launch-shape
+// choice and launches of ds_cache_quantize, ds_sparse_attention_q8,
+// ds_attention_mass, ds_cache_evict and ds_cache_compact.  Included by lib.cu
+// after its helpers (device_state, set_pdl, wait_limit).  None of these
+// allocates or keeps anything: calls on different streams may overlap.
+#pragma once
+
+namespace dstopk {
+
+static bool cache_misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+// log2 of a block size (1, 2, 4 .. DS_CACHE_MAX_BLOCK), or -1.
+static int cache_log_block(int block) {
+  for (int l = 0; (1 << l) <= DS_CACHE_MAX_BLOCK; ++l)
+    if (block == 1 << l) return l;
+  return -1;
+}
+
+static bool cache_is8(int dtype) { return dtype == DS_E4M3 || dtype == DS_I8; }
+
+// One launch, chained to the kernel before it by programmatic dependent launch.
+template <class P>
+static int cache_launch(void (*kern)(P), const P& p, dim3 grid, int threads, size_t smem, void* stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  set_pdl(attr[0]);
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_on() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? DS_OK : DS_ERR_CUDA;
+}
+
+// The arguments that the attention and the account share.
+static int cache_attn_check(const void* q, const void* cache, int64_t cache_batch_stride, const float* scales,
+                            int64_t scales_batch_stride, int dtype, int block, int T, const int32_t* idx, int k,
+                            int batch, int heads, int kv_heads, int d, float scale) {
+  if (!q || !cache || batch < 1 || batch > 65535 || T < 1 || k < 0 || k > DS_MAX_K || (k > 0 && !idx)) return DS_ERR_ARG;
+  if (heads < 1 || heads > DS_ATTN_MAX_HEADS || kv_heads < 1 || heads % kv_heads != 0) return DS_ERR_ARG;
+  if (d < 64 || d > DS_ATTN_MAX_DIM || d % 64 != 0 || !std::isfinite(scale)) return DS_ERR_ARG;
+  if (cache_batch_stride < 0 || cache_misaligned(q, 16) || cache_misaligned(cache, 16) || cache_misaligned(idx, 4))
+    return DS_ERR_ARG;
+  if (cache_is8(dtype)) {
+    if (!scales || cache_misaligned(scales, 4) || scales_batch_stride < 0 || cache_log_block(block) < 0) return DS_ERR_ARG;
+  } else if (dtype != DS_BF16 || scales) {
+    return DS_ERR_ARG;
+  }
+  return DS_OK;
+}
+
+}  // namespace dstopk
+
+extern "C" int ds_cache_quantize(const void* rows, int64_t rows_batch_stride, int64_t row_stride, int batch, int n,
+                                 int kv_heads, int d, int dtype, int block, const int32_t* pos, const int32_t* len,
+                                 void* codes, int64_t codes_batch_stride, float* scales, int64_t scales_batch_stride,
+                                 int T, void* stream) {
+  const int lb = cache_log_block(block);
+  if (!rows || !codes || !scales || batch < 1 || batch > 65535 || n < 1 || T < 1 || lb < 0 || !cache_is8(dtype))
+    return DS_ERR_ARG;
+  if (kv_heads < 1 || kv_heads > DS_ATTN_MAX_HEADS || d < 64 || d > DS_ATTN_MAX_DIM || d % 64 != 0) return DS_ERR_ARG;
+  const int64_t width = (int64_t)kv_heads * d;
+  if (row_stride < width || row_stride % 8 != 0 || rows_batch_stride < 0 || rows_batch_stride % 8 != 0) return DS_ERR_ARG;
+  const int64_t nb = ((int64_t)T + block - 1) / block;
+  if (batch > 1 && (codes_batch_stride < T || scales_batch_stride < nb)) return DS_ERR_ARG;
+  if (cache_misaligned(rows, 16) || cache_misaligned(codes, 16) || cache_misaligned(scales, 4) ||
+      cache_misaligned(pos, 4) || cache_misaligned(len, 4))
+    return DS_ERR_ARG;
+  CqParams p = {};
+  p.nblocks = (int)(((int64_t)n + block - 1) / block);
+  const int64_t units = (int64_t)p.nblocks * kv_heads * batch;
+  if (units > INT32_MAX) return DS_ERR_ARG;
+  DeviceState* s = nullptr;
+  const int rc = device_state(&s);
+  if (rc != DS_OK) return rc;
+  p.rows = static_cast<const uint16_t*>(rows);
+  p.codes = static_cast<uint8_t*>(codes);
+  p.scales = scales;
+  p.pos = pos;
+  p.len = len;
+  p.status = s->status;
+  p.rows_bstride = rows_batch_stride;
+  p.rows_rstride = row_stride;
+  p.codes_bstride = codes_batch_stride * width;
+  p.scales_bstride = scales_batch_stride * kv_heads;
+  p.n = n;
+  p.Hkv = kv_heads;
+  p.D = d;
+  p.T = T;
+  p.log_block = lb;
+  return cache_launch(dtype == DS_E4M3 ? cache_quantize_kernel<kFmtE4m3> : cache_quantize_kernel<kFmtI8>, p,
+                      dim3((unsigned)units), 256, 0, stream);
+}
+
+extern "C" int ds_sparse_attention_q8(const void* q, const void* codes, int64_t codes_batch_stride, const float* scales,
+                                      int64_t scales_batch_stride, int dtype, int block, int T, const int32_t* idx,
+                                      int k, const void* win, int W, const int32_t* win_len, const float* sink,
+                                      int batch, int heads, int kv_heads, int d, float scale, void* out, float* lse,
+                                      void* stream) {
+  int rc = cache_attn_check(q, codes, codes_batch_stride, scales, scales_batch_stride, dtype, block, T, idx, k, batch,
+                            heads, kv_heads, d, scale);
+  if (rc != DS_OK) return rc;
+  if (!cache_is8(dtype) || !out || W < 0 || W > DS_ATTN_MAX_WINDOW || (W > 0 && !win)) return DS_ERR_ARG;
+  if (cache_misaligned(out, 16) || cache_misaligned(win, 16) || cache_misaligned(win_len, 4) ||
+      cache_misaligned(sink, 4) || cache_misaligned(lse, 4))
+    return DS_ERR_ARG;
+  DeviceState* s = nullptr;
+  rc = device_state(&s);
+  if (rc != DS_OK) return rc;
+  AqParams p = {};
+  p.q = static_cast<const uint16_t*>(q);
+  p.cache = static_cast<const uint8_t*>(codes);
+  p.scales = scales;
+  p.win = static_cast<const uint16_t*>(win);
+  p.idx = idx;
+  p.win_len = win_len;
+  p.sink = sink;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.status = s->status;
+  p.wait_ns = wait_limit();
+  p.cache_bstride = codes_batch_stride * kv_heads * d;
+  p.scales_bstride = scales_batch_stride * kv_heads;
+  p.T = T;
+  p.k = k;
+  p.W = W;
+  p.B = batch;
+  p.H = heads;
+  p.Hkv = kv_heads;
+  p.D = d;
+  p.log_block = cache_log_block(block);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  return cache_launch(dtype == DS_E4M3 ? attn_q8_kernel<kFmtE4m3> : attn_q8_kernel<kFmtI8>, p,
+                      dim3((unsigned)(batch * heads)), 256, (size_t)(k + W) * 4, stream);
+}
+
+extern "C" int ds_attention_mass(const void* q, const void* cache, int64_t cache_batch_stride, const float* scales,
+                                 int64_t scales_batch_stride, int dtype, int block, int T, const int32_t* idx, int k,
+                                 const float* lse, int batch, int heads, int kv_heads, int d, float scale, float* mass,
+                                 int64_t mass_batch_stride, void* stream) {
+  int rc = cache_attn_check(q, cache, cache_batch_stride, scales, scales_batch_stride, dtype, block, T, idx, k, batch,
+                            heads, kv_heads, d, scale);
+  if (rc != DS_OK) return rc;
+  if (!lse || !mass || (batch > 1 && mass_batch_stride < T) || cache_misaligned(lse, 4) || cache_misaligned(mass, 4))
+    return DS_ERR_ARG;
+  DeviceState* s = nullptr;
+  rc = device_state(&s);
+  if (rc != DS_OK || k == 0) return rc;
+  AqParams p = {};
+  p.q = static_cast<const uint16_t*>(q);
+  p.cache = static_cast<const uint8_t*>(cache);
+  p.scales = scales;
+  p.idx = idx;
+  p.lse = const_cast<float*>(lse);
+  p.mass = mass;
+  p.status = s->status;
+  p.wait_ns = wait_limit();
+  p.cache_bstride = cache_batch_stride * kv_heads * d;
+  p.scales_bstride = scales_batch_stride * kv_heads;
+  p.mass_bstride = mass_batch_stride;
+  p.T = T;
+  p.k = k;
+  p.B = batch;
+  p.H = heads;
+  p.Hkv = kv_heads;
+  p.D = d;
+  p.log_block = cache_is8(dtype) ? cache_log_block(block) : 0;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  return cache_launch(dtype == DS_BF16   ? attn_mass_kernel<kFmtBf16>
+                      : dtype == DS_E4M3 ? attn_mass_kernel<kFmtE4m3>
+                                         : attn_mass_kernel<kFmtI8>,
+                      p, dim3((unsigned)(((int64_t)batch * k + 7) / 8)), 256, 0, stream);
+}
+
+extern "C" int ds_cache_evict(const float* mass, int64_t mass_batch_stride, int batch, int T, const int32_t* len,
+                              int block, int budget, int keep_first, int keep_last, int32_t* kept, int32_t* new_len,
+                              void* stream) {
+  if (!mass || !kept || !new_len || batch < 1 || batch > 65535 || T < 1 || T > kMaxRowElems || mass_batch_stride < 0)
+    return DS_ERR_ARG;
+  if (cache_log_block(block) < 0 || budget < 1 || budget > (T + block - 1) / block || keep_first < 0 || keep_last < 0 ||
+      keep_first > budget || keep_last > budget - keep_first)
+    return DS_ERR_ARG;
+  if (cache_misaligned(mass, 4) || cache_misaligned(len, 4) || cache_misaligned(kept, 4) || cache_misaligned(new_len, 4))
+    return DS_ERR_ARG;
+  DeviceState* s = nullptr;
+  const int rc = device_state(&s);
+  if (rc != DS_OK) return rc;
+  CeParams p = {};
+  p.mass = mass;
+  p.len = len;
+  p.kept = kept;
+  p.new_len = new_len;
+  p.status = s->status;
+  p.mass_bstride = mass_batch_stride;
+  p.T = T;
+  p.block = block;
+  p.budget = budget;
+  p.first = keep_first;
+  p.last = keep_last;
+  return cache_launch(cache_evict_kernel, p, dim3((unsigned)batch), 1024, 0, stream);
+}
+
+extern "C" int ds_cache_compact(const ds_cache_array* arrays, int n_arrays, const int32_t* kept, int budget,
+                                const int32_t* len, int batch, int T, int block, void* stream) {
+  if (!arrays || !kept || n_arrays < 1 || n_arrays > DS_CACHE_MAX_ARRAYS || batch < 1 || batch > 65535 || T < 1 ||
+      T > kMaxRowElems || cache_log_block(block) < 0)
+    return DS_ERR_ARG;
+  const int64_t nb = ((int64_t)T + block - 1) / block;
+  if (budget < 1 || budget > nb || cache_misaligned(kept, 4) || cache_misaligned(len, 4)) return DS_ERR_ARG;
+  if ((int64_t)batch * budget > INT32_MAX) return DS_ERR_ARG;
+  CcParams p = {};
+  for (int i = 0; i < n_arrays; ++i) {
+    const ds_cache_array& a = arrays[i];
+    if (!a.src || !a.dst || a.item_bytes < 1 || a.item_bytes > (int64_t(1) << 24) || (a.per_block != 0 && a.per_block != 1))
+      return DS_ERR_ARG;
+    const int64_t src_bytes = a.item_bytes * (a.per_block ? nb : T);
+    const int64_t dst_bytes = a.item_bytes * (a.per_block ? budget : std::min<int64_t>(T, (int64_t)budget * block));
+    if (batch > 1 && (a.src_batch_stride < src_bytes || a.dst_batch_stride < dst_bytes)) return DS_ERR_ARG;
+    // the moves are not ordered among themselves, so the buffers may not overlap
+    const uintptr_t s0 = reinterpret_cast<uintptr_t>(a.src), d0 = reinterpret_cast<uintptr_t>(a.dst);
+    const uintptr_t s1 = s0 + (uintptr_t)((batch - 1) * a.src_batch_stride + src_bytes);
+    const uintptr_t d1 = d0 + (uintptr_t)((batch - 1) * a.dst_batch_stride + dst_bytes);
+    if (s0 < d1 && d0 < s1) return DS_ERR_ARG;
+    const uint64_t bits = (uint64_t)s0 | d0 | (uint64_t)a.item_bytes |
+                          (batch > 1 ? (uint64_t)a.src_batch_stride | (uint64_t)a.dst_batch_stride : 0);
+    CcArray& c = p.a[i];
+    c.src = static_cast<const uint8_t*>(a.src);
+    c.dst = static_cast<uint8_t*>(a.dst);
+    c.src_bstride = a.src_batch_stride;
+    c.dst_bstride = a.dst_batch_stride;
+    c.item = a.item_bytes;
+    c.per_block = a.per_block;
+    c.vec = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
+  }
+  DeviceState* s = nullptr;
+  const int rc = device_state(&s);
+  if (rc != DS_OK) return rc;
+  p.kept = kept;
+  p.len = len;
+  p.status = s->status;
+  p.T = T;
+  p.block = block;
+  p.budget = budget;
+  p.n = n_arrays;
+  return cache_launch(cache_compact_kernel, p, dim3((unsigned)(batch * budget)), 256, 0, stream);
+}

@@ -3,6 +3,8 @@
 // unit holds every kernel, so device symbols (the status word) resolve here.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
+#include <cstdint>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -20,6 +22,9 @@
 #include "attention_kernel.cuh"
 #include "qproj_kernel.cuh"
 #include "compress_kernel.cuh"
+#include "cache_quant_kernel.cuh"
+#include "attention_q8_kernel.cuh"
+#include "cache_evict_kernel.cuh"
 
 namespace dstopk {
 
@@ -1172,3 +1177,5 @@ extern "C" int ds_compress_fold(const void* rows, int batch, int D, int64_t rows
   cfg.numAttrs = pdl_on() ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, compress_fold_kernel, p) == cudaSuccess ? DS_OK : DS_ERR_CUDA;
 }
+
+#include "cache_ops.cuh"

@@ -27,6 +27,11 @@ Workloads (sizes and distributions of the selection step's headline cases):
                       length ~ U{4096..32768}, a window of 128 rows, and one
                       sink logit per head; values ~ N(0, 1).
 
+* ``cache_rows``      rows to be cached: unit normal, every row at a level of its own
+                      (a factor e^N(0, 0.3^2)), as [B, n, kv_heads, d] bfloat16.
+* ``cache_slots``     distinct selected rows per batch row, a fraction of them skipped.
+* ``accounts``        accumulated attention weights with a long tail, e^N(0, 2^2).
+
 bfloat16 values are produced by drawing float32 samples and rounding them to
 the nearest bfloat16, ties to even, and are returned as uint16 bit patterns.
 """
@@ -202,3 +207,30 @@ def compress(seed=SEED_COMPRESS, batch=8, D=512, gate_scale=1.0):
     rows = f32_to_bf16_bits(g.standard_normal((batch, 4, D), dtype=np.float32))
     gate = f32_to_bf16_bits(g.standard_normal(D, dtype=np.float32) * np.float32(gate_scale / np.sqrt(D)))
     return rows, gate
+
+
+def cache_rows(seed, batch, n, kv_heads, d):
+    """bfloat16 patterns [batch, n, kv_heads, d] of unit normal rows, each at a level of its own."""
+    g = rng(seed)
+    x = g.standard_normal((batch, n, kv_heads, d), dtype=np.float32)
+    level = np.exp(np.float32(0.3) * g.standard_normal((batch, n, kv_heads, 1), dtype=np.float32))
+    return f32_to_bf16_bits(x * level)
+
+
+def cache_slots(seed, batch, T, k, holes=0.0):
+    """int32 [batch, k]: distinct rows below T (-1 where k exceeds T); a fraction
+    ``holes`` replaced by -1 or by rows at or past T."""
+    g = rng(seed)
+    idx = np.full((batch, k), -1, dtype=np.int32)
+    for b in range(batch):
+        m = min(k, T)
+        idx[b, :m] = g.choice(T, size=m, replace=False)
+    if holes > 0 and k > 0:
+        bad = np.where(g.random((batch, k)) < 0.5, -1, T + g.integers(0, 1000, size=(batch, k)))
+        idx = np.where(g.random((batch, k)) < holes, bad, idx).astype(np.int32)
+    return idx
+
+
+def accounts(seed, batch, T):
+    """float32 [batch, T] accumulated attention weights with a long tail."""
+    return np.exp(2.0 * rng(seed).standard_normal((batch, T))).astype(np.float32)

@@ -1,0 +1,104 @@
+"""The C entry points of the 8-bit cache answer bad arguments on the host, and the
+Python front end refuses tensors that are not on a GPU (CPU only)."""
+
+import ctypes
+
+import pytest
+import torch
+
+import sparse_attention_top_ds_b200 as ds
+from sparse_attention_top_ds_b200 import _native
+
+A = ctypes.c_void_p(0x100000)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from sparse_attention_top_ds_b200 import build
+    build.build()
+    return ds.load()
+
+
+def odd(n):
+    return ctypes.c_void_p(0x100000 + n)
+
+
+def test_quantize_arguments(lib):
+    def call(rows=A, bs=0, rs=512, batch=2, n=10, heads=1, d=512, dtype=2, block=16, pos=None, length=None, codes=A, cs=100,
+             scales=A, ss=7, T=100):
+        return lib.ds_cache_quantize(rows, bs, rs, batch, n, heads, d, dtype, block, pos, length, codes, cs, scales, ss, T, None)
+
+    for bad in (dict(rows=None), dict(codes=None), dict(scales=None), dict(batch=0), dict(batch=65536), dict(n=0), dict(T=0),
+                dict(heads=0), dict(heads=4097, rs=4097 * 512), dict(d=0), dict(d=100), dict(d=576), dict(dtype=0), dict(dtype=1),
+                dict(dtype=4), dict(block=0), dict(block=3), dict(block=256), dict(block=-1), dict(rs=511), dict(rs=516),
+                dict(bs=-8), dict(bs=4), dict(cs=99), dict(ss=6), dict(rows=odd(8)), dict(codes=odd(4)), dict(scales=odd(2)),
+                dict(pos=odd(1)), dict(length=odd(2)), dict(batch=65535, n=2 ** 31 - 1, block=1)):
+        assert call(**bad) == ds.DS_ERR_ARG, bad
+
+
+def test_attention_arguments(lib):
+    def call(q=A, codes=A, cs=0, scales=A, ss=0, dtype=2, block=16, T=100, idx=A, k=10, win=None, W=0, wl=None, sink=None, batch=2,
+             heads=128, kv=1, d=512, scale=0.04, out=A, lse=None):
+        return lib.ds_sparse_attention_q8(q, codes, cs, scales, ss, dtype, block, T, idx, k, win, W, wl, sink, batch, heads, kv, d,
+                                          scale, out, lse, None)
+
+    for bad in (dict(q=None), dict(codes=None), dict(scales=None), dict(out=None), dict(cs=-1), dict(ss=-1), dict(dtype=1),
+                dict(dtype=1, scales=None), dict(dtype=0), dict(block=0), dict(block=12), dict(block=256), dict(T=0), dict(idx=None),
+                dict(k=-1), dict(k=2049), dict(W=-1), dict(W=8), dict(W=4097, win=A), dict(batch=0), dict(batch=65536), dict(heads=0),
+                dict(heads=4097), dict(kv=0), dict(kv=3), dict(kv=256), dict(d=32), dict(d=100), dict(d=576),
+                dict(scale=float("nan")), dict(scale=float("inf")), dict(q=odd(8)), dict(codes=odd(8)), dict(scales=odd(1)),
+                dict(idx=odd(2)), dict(win=odd(8), W=4), dict(wl=odd(2)), dict(sink=odd(2)), dict(out=odd(8)), dict(lse=odd(2))):
+        assert call(**bad) == ds.DS_ERR_ARG, bad
+
+
+def test_mass_arguments(lib):
+    def call(q=A, cache=A, cs=0, scales=A, ss=0, dtype=2, block=16, T=100, idx=A, k=10, lse=A, batch=2, heads=128, kv=1, d=512,
+             scale=0.04, mass=A, ms=100):
+        return lib.ds_attention_mass(q, cache, cs, scales, ss, dtype, block, T, idx, k, lse, batch, heads, kv, d, scale, mass, ms,
+                                     None)
+
+    for bad in (dict(lse=None), dict(mass=None), dict(ms=99), dict(ms=0), dict(lse=odd(2)), dict(mass=odd(1)), dict(q=None),
+                dict(cache=None), dict(scales=None), dict(dtype=1), dict(dtype=0, scales=None), dict(block=5), dict(k=2049),
+                dict(idx=None), dict(kv=7), dict(d=72), dict(T=0), dict(batch=0), dict(cs=-1), dict(scale=float("inf"))):
+        assert call(**bad) == ds.DS_ERR_ARG, bad
+
+
+def test_evict_arguments(lib):
+    def call(mass=A, ms=100, batch=2, T=100, length=None, block=16, budget=4, first=1, last=1, kept=A, new_len=A):
+        return lib.ds_cache_evict(mass, ms, batch, T, length, block, budget, first, last, kept, new_len, None)
+
+    for bad in (dict(mass=None), dict(kept=None), dict(new_len=None), dict(ms=-1), dict(batch=0), dict(batch=65536), dict(T=0),
+                dict(T=(1 << 24) + 1), dict(block=0), dict(block=24), dict(block=256), dict(budget=0), dict(budget=8),
+                dict(first=-1), dict(last=-1), dict(first=5, last=0), dict(first=2, last=3), dict(first=2 ** 31 - 1, last=2 ** 31 - 1),
+                dict(mass=odd(2)), dict(length=odd(2)), dict(kept=odd(1)), dict(new_len=odd(2))):
+        assert call(**bad) == ds.DS_ERR_ARG, bad
+
+
+def test_compact_arguments(lib):
+    def call(n=1, kept=A, budget=4, length=None, batch=2, T=100, block=16, arrays=True, **a):
+        f = dict(src=0x100000, dst=0x900000, src_batch_stride=102400, dst_batch_stride=65536, item_bytes=1024, per_block=0)
+        f.update(a)
+        arr = (_native._CacheArray * max(1, min(n, 9)))()
+        for i in range(len(arr)):
+            arr[i] = _native._CacheArray(**f)
+        return lib.ds_cache_compact(arr if arrays else None, n, kept, budget, length, batch, T, block, None)
+
+    for bad in (dict(arrays=False), dict(n=0), dict(n=9), dict(kept=None), dict(budget=0), dict(budget=8), dict(batch=0),
+                dict(batch=65536), dict(T=0), dict(T=(1 << 24) + 1), dict(block=3), dict(kept=odd(2)), dict(length=odd(1)),
+                dict(src=None), dict(dst=None), dict(item_bytes=0), dict(item_bytes=(1 << 24) + 1), dict(per_block=2),
+                dict(src_batch_stride=102399), dict(dst_batch_stride=65535),
+                dict(dst=0x100000), dict(dst=0x100000 + 102400 + 102399), dict(src=0x900000 + 65536 + 65535)):  # overlaps
+        assert call(**bad) == ds.DS_ERR_ARG, bad
+
+
+def test_front_end_refuses_tensors_off_the_gpu():
+    x = torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16)
+    codes, scales = torch.zeros(2, 8, 1, 64, dtype=torch.int8), torch.zeros(2, 8, 1)
+    q, idx, lse = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 4)
+    for f in (lambda: ds.ds_cache_quantize(x, codes, scales, 1), lambda: ds.ds_sparse_attention_q8(q, codes, scales, idx, 1),
+              lambda: ds.ds_attention_mass(q, codes, idx, lse, torch.zeros(2, 8), scales=scales),
+              lambda: ds.ds_cache_evict(torch.zeros(2, 8), 4), lambda: ds.ds_cache_compact(idx)):
+        with pytest.raises(ValueError):
+            f()
+    with pytest.raises(TypeError):
+        ds.ds_cache_evict(None, 4)
