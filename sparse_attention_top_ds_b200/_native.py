@@ -483,125 +483,136 @@ def ds_compress_fold(rows, gate, out=None, stream=None):
 # Given another stream, what they return is allocated on it, and every tensor is
 # recorded there, so that freeing a tensor does not hand out its memory early;
 # the caller orders the two streams, as for any other work.
+#
+# A decode step makes several of these calls per layer, so the usual call (the
+# current stream, contiguous tensors) passes each check in one comparison; the
+# reason for a refusal is worked out only once there is one.
 
-class _Call:
-    """Where a call runs: the tensors' device, and the stream."""
-
-    __slots__ = ("dev", "stream", "other", "tensors")
-
-    def __init__(self, dev, stream):
-        import torch
-        cur = torch.cuda.current_stream(dev)
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, expected {dev}")
-        self.dev = dev
-        self.stream = cur if stream is None else stream
-        self.other = cur if stream is not None and stream != cur else None
-        self.tensors = []
-
-    def need(self, t, dtype, name, shape=None, optional=False):
-        """Check an argument; shape entries of None match anything."""
-        import torch
-        if t is None and optional:
-            return None
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.device != self.dev:
-            raise ValueError(f"{name} is on {t.device}, expected {self.dev}")
-        if dtype is not None and t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if shape is not None and (t.dim() != len(shape) or any(e is not None and e != n for e, n in zip(shape, t.shape))):
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        if self.other is not None:
-            self.tensors.append(t)
-        return t
-
-    def empty(self, shape, dtype):
-        import torch
-        if self.other is None:
-            return torch.empty(shape, dtype=dtype, device=self.dev)
-        with torch.cuda.stream(self.stream):
-            t = torch.empty(shape, dtype=dtype, device=self.dev)
-        t.record_stream(self.other)
-        return t
-
-    def run(self, where, fn, *args):
-        import torch
-        if torch.cuda.current_device() == self.dev.index:
-            rc = fn(*args, self.stream.cuda_stream)
-        else:
-            with torch.cuda.device(self.dev):
-                rc = fn(*args, self.stream.cuda_stream)
-        for t in self.tensors:
-            t.record_stream(self.stream)
-        _check(rc, where)
+def _refuse(t, dtype, shape, dev, name):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
+def _arg(t, dtype, shape, dev, name):
+    """Address of a contiguous tensor argument."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, dtype, shape, dev, name)
 
 
-def _cuda_device(t, name):
+def _opt(t, dtype, shape, dev, name):
+    return None if t is None else _arg(t, dtype, shape, dev, name)
+
+
+def _rows_arg(t, dtype, shape, dev, name, lead=1):
+    """Address of an argument that is contiguous behind its first ``lead``
+    dimensions (sizes of one have no stride)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == dev:
+            if not t.is_contiguous():
+                step = 1
+                for n, st in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
+                    if n != 1 and st != step:
+                        raise ValueError(f"{name} must be contiguous behind dimension {lead}")
+                    step *= n
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, dtype, shape, dev, name)
+
+
+def _batch_step(t, unit, name):
+    """Batch stride of t [batch, ...] in units of ``unit`` elements."""
+    st = t.stride(0) if t.shape[0] > 1 else t[0].numel()
+    if st % unit:
+        raise ValueError(f"{name}: the batch stride must be whole rows")
+    return st // unit
+
+
+def _lead(t, dims, name):
+    """Device of the argument that says where a call runs."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {list(t.shape)}")
     return t.device
 
 
-def _dense(t, name, lead=1):
-    """t is contiguous behind its first ``lead`` dimensions (sizes of one have no stride)."""
-    step = 1
-    for n, st in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
-        if n != 1 and st != step:
-            raise ValueError(f"{name} must be contiguous behind dimension {lead}")
-        step *= n
+def _new(shape, dtype, dev, stream):
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    here = torch.cuda.current_stream(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, expected {dev}")
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if here != stream:
+        t.record_stream(here)
     return t
 
 
-def _steps(t, unit, name):
-    """Batch stride of t [batch, ...] in units of ``unit`` elements."""
-    if t.shape[0] == 1:
-        return t[0].numel() // unit
-    if t.stride(0) % unit:
-        raise ValueError(f"{name}: the batch stride must be whole rows")
-    return t.stride(0) // unit
-
-
-def _cache8_dtype(t, name):
+def _run(where, fn, args, dev, stream, tensors):
     import torch
-    if t.dtype == torch.float8_e4m3fn:
-        return DS_E4M3
-    if t.dtype == torch.int8:
-        return DS_I8
-    raise TypeError(f"{name} must be torch.float8_e4m3fn or torch.int8, got {t.dtype}")
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, expected {dev}")
+    else:
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, raw)
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+    if rc != DS_OK:
+        raise DsError(rc, where)
 
 
-def _cache8(call, codes, scales, block, batch):
-    """(dtype, T, kv_heads, d, code rows, scale blocks from one batch row to the next)."""
-    call.need(codes, None, "codes")
-    dt = _cache8_dtype(codes, "codes")
+def _cache8(codes, scales, block, batch, dev):
+    """(dtype, T, kv_heads, d, addresses and batch strides) of an 8-bit cache."""
+    import torch
+    if not isinstance(codes, torch.Tensor):
+        raise TypeError("codes must be a torch.Tensor")
+    if codes.dtype is torch.float8_e4m3fn:
+        dt = DS_E4M3
+    elif codes.dtype is torch.int8:
+        dt = DS_I8
+    else:
+        raise TypeError(f"codes must be torch.float8_e4m3fn or torch.int8, got {codes.dtype}")
     if not isinstance(block, int) or block < 1:
         raise ValueError("block must be a positive int")
-    if codes.dim() not in (3, 4) or (codes.dim() == 4 and codes.shape[0] != batch):
-        raise ValueError("codes must be [T, kv_heads, d] or [batch, T, kv_heads, d]")
-    T, kv_heads, d = codes.shape[-3:]
-    nb, f32 = (T + block - 1) // block, _torch().float32
-    if codes.dim() == 3:
-        call.need(scales, f32, "scales", (nb, kv_heads))
-        _dense(codes, "codes", 0), _dense(scales, "scales", 0)
-        strides = 0, 0
-    else:
-        call.need(scales, f32, "scales", (batch, nb, kv_heads))
-        _dense(codes, "codes"), _dense(scales, "scales")
-        strides = _steps(codes, max(1, kv_heads * d), "codes"), _steps(scales, max(1, kv_heads), "scales")
-    return (dt, T, kv_heads, d) + strides
-
-
-def _torch():
-    import torch
-    return torch
+    shape = codes.shape
+    if len(shape) == 4 and shape[0] == batch:
+        _, T, kv_heads, d = shape
+        nb = (T + block - 1) // block
+        c = _rows_arg(codes, codes.dtype, shape, dev, "codes")
+        s = _rows_arg(scales, torch.float32, (batch, nb, kv_heads), dev, "scales")
+        return dt, T, kv_heads, d, c, _batch_step(codes, max(1, kv_heads * d), "codes"), s, _batch_step(
+            scales, max(1, kv_heads), "scales")
+    if len(shape) == 3:
+        T, kv_heads, d = shape
+        c = _arg(codes, codes.dtype, shape, dev, "codes")
+        return dt, T, kv_heads, d, c, 0, _arg(scales, torch.float32, ((T + block - 1) // block, kv_heads), dev, "scales"), 0
+    raise ValueError(f"codes must be [T, kv_heads, d] or [{batch}, T, kv_heads, d], got {list(shape)}")
 
 
 def ds_cache_quantize(rows, codes, scales, block, pos=None, length=None, stream=None):
@@ -615,22 +626,17 @@ def ds_cache_quantize(rows, codes, scales, block, pos=None, length=None, stream=
     length  int32 [batch] or None (= n): how many rows are written.
     Returns (codes, scales).
     """
-    torch = _torch()
-    call = _Call(_cuda_device(rows, "rows"), stream)
-    call.need(rows, torch.bfloat16, "rows", (None, None, None, None))
+    import torch
+    dev = _lead(rows, 4, "rows")
     batch, n, kv_heads, d = rows.shape
-    dt, T, ch, cd, cstep, sstep = _cache8(call, codes, scales, block, batch)
-    if codes.dim() != 4 or (ch, cd) != (kv_heads, d):
+    dt, T, ch, cd, c, cstep, s, sstep = _cache8(codes, scales, block, batch, dev)
+    if ch != kv_heads or cd != d or codes.dim() != 4:
         raise ValueError("codes must be [batch, T, kv_heads, d] with the rows' kv_heads and d")
-    _dense(rows, "rows", 2)
-    call.need(pos, torch.int32, "pos", (batch,), optional=True)
-    call.need(length, torch.int32, "length", (batch,), optional=True)
-    for t, name in ((pos, "pos"), (length, "length")):
-        if t is not None:
-            _dense(t, name, 0)
-    call.run("ds_cache_quantize", load().ds_cache_quantize, _at(rows), rows.stride(0) if batch > 1 else 0,
-             rows.stride(1) if n > 1 else kv_heads * d, batch, n, kv_heads, d, dt, block, _at(pos), _at(length),
-             _at(codes), cstep, _at(scales), sstep, T)
+    x = _rows_arg(rows, torch.bfloat16, rows.shape, dev, "rows", 2)
+    args = (x, rows.stride(0) if batch > 1 else 0, rows.stride(1) if n > 1 else kv_heads * d, batch, n, kv_heads, d, dt, block,
+            _opt(pos, torch.int32, (batch,), dev, "pos"), _opt(length, torch.int32, (batch,), dev, "length"), c, cstep, s,
+            sstep, T)
+    _run("ds_cache_quantize", load().ds_cache_quantize, args, dev, stream, (rows, codes, scales, pos, length))
     return codes, scales
 
 
@@ -648,32 +654,31 @@ def ds_sparse_attention_q8(q, codes, scales, idx, block, scale=None, win=None, w
     Query head h reads KV head h // (heads // kv_heads).
     Returns out bf16 [batch, heads, d], or (out, lse float32 [batch, heads]).
     """
-    torch = _torch()
-    call = _Call(_cuda_device(q, "q"), stream)
-    call.need(q, torch.bfloat16, "q", (None, None, None))
-    batch, heads, d = q.shape
-    dt, T, kv_heads, cd, cstep, sstep = _cache8(call, codes, scales, block, batch)
+    import torch
+    dev = _lead(q, 3, "q")
+    batch, heads, d = shape = q.shape
+    dt, T, kv_heads, cd, c, cstep, s, sstep = _cache8(codes, scales, block, batch, dev)
     if cd != d:
         raise ValueError("codes and q differ in d")
-    call.need(idx, torch.int32, "idx", (batch, None), optional=True)
-    call.need(win, torch.bfloat16, "win", (batch, None, kv_heads, d), optional=True)
-    call.need(win_len, torch.int32, "win_len", (batch,), optional=True)
-    call.need(sink, torch.float32, "sink", (heads,), optional=True)
-    k, W = 0 if idx is None else idx.shape[1], 0 if win is None else win.shape[1]
+    qp = _arg(q, torch.bfloat16, shape, dev, "q")
+    k = W = 0
+    ip = wp = None
+    if idx is not None:
+        k = idx.shape[-1]
+        ip = _arg(idx, torch.int32, (batch, k), dev, "idx") if k else None
+    if win is not None:
+        W = win.shape[1]
+        wp = _arg(win, torch.bfloat16, (batch, W, kv_heads, d), dev, "win") if W else None
+    lp, sp = _opt(win_len, torch.int32, (batch,), dev, "win_len"), _opt(sink, torch.float32, (heads,), dev, "sink")
     if out is None:
-        out = call.empty((batch, heads, d), torch.bfloat16)
-    else:
-        call.need(out, torch.bfloat16, "out", (batch, heads, d))
-    if lse is not None:
-        call.need(lse, torch.float32, "lse", (batch, heads))
-    elif return_lse:
-        lse = call.empty((batch, heads), torch.float32)
-    for t, name in ((q, "q"), (idx, "idx"), (win, "win"), (win_len, "win_len"), (sink, "sink"), (out, "out"), (lse, "lse")):
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    call.run("ds_sparse_attention_q8", load().ds_sparse_attention_q8, _at(q), _at(codes), cstep, _at(scales), sstep, dt,
-             block, T, _at(idx) if k else None, k, _at(win) if W else None, W, _at(win_len), _at(sink), batch, heads,
-             kv_heads, d, 1.0 / math.sqrt(d) if scale is None else float(scale), _at(out), _at(lse))
+        out = _new(shape, torch.bfloat16, dev, stream)
+    if lse is None and return_lse:
+        lse = _new((batch, heads), torch.float32, dev, stream)
+    args = (qp, c, cstep, s, sstep, dt, block, T, ip, k, wp, W, lp, sp, batch, heads, kv_heads, d,
+            d ** -0.5 if scale is None else float(scale), _arg(out, torch.bfloat16, shape, dev, "out"),
+            _opt(lse, torch.float32, (batch, heads), dev, "lse"))
+    _run("ds_sparse_attention_q8", load().ds_sparse_attention_q8, args, dev, stream,
+         (q, codes, scales, idx, win, win_len, sink, out, lse))
     return (out, lse) if return_lse else out
 
 
@@ -688,33 +693,27 @@ def ds_attention_mass(q, cache, idx, lse, mass, scales=None, block=1, scale=None
     mass   float32 [batch, T], rows contiguous.
     Returns mass.
     """
-    torch = _torch()
-    call = _Call(_cuda_device(q, "q"), stream)
-    call.need(q, torch.bfloat16, "q", (None, None, None))
-    batch, heads, d = q.shape
+    import torch
+    dev = _lead(q, 3, "q")
+    batch, heads, d = shape = q.shape
     if scales is not None:
-        dt, T, kv_heads, cd, cstep, sstep = _cache8(call, cache, scales, block, batch)
+        dt, T, kv_heads, cd, c, cstep, s, sstep = _cache8(cache, scales, block, batch, dev)
     else:
-        call.need(cache, torch.bfloat16, "cache")
-        if cache.dim() not in (2, 3, 4) or (cache.dim() > 2 and cache.shape[0] != batch):
+        if not isinstance(cache, torch.Tensor) or cache.dim() not in (2, 3, 4) or (cache.dim() > 2 and cache.shape[0] != batch):
             raise ValueError("a bf16 cache must be [T, d], [batch, T, d] or [batch, T, kv_heads, d]")
         T, kv_heads = (cache.shape[1], cache.shape[2]) if cache.dim() == 4 else (cache.shape[-2], 1)
-        dt, cd, sstep, block = DS_BF16, cache.shape[-1], 0, 1
-        _dense(cache, "cache", 0 if cache.dim() == 2 else 1)
-        cstep = 0 if cache.dim() == 2 else _steps(cache, max(1, kv_heads * cd), "cache")
+        dt, cd, s, sstep, block = DS_BF16, cache.shape[-1], None, 0, 1
+        c = _rows_arg(cache, torch.bfloat16, cache.shape, dev, "cache", 0 if cache.dim() == 2 else 1)
+        cstep = 0 if cache.dim() == 2 else _batch_step(cache, max(1, kv_heads * cd), "cache")
     if cd != d:
         raise ValueError("cache and q differ in d")
-    call.need(idx, torch.int32, "idx", (batch, None))
-    call.need(lse, torch.float32, "lse", (batch, heads))
-    call.need(mass, torch.float32, "mass", (batch, T))
-    for t, name in ((q, "q"), (idx, "idx"), (lse, "lse")):
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    _dense(mass, "mass")
-    k = idx.shape[1]
-    call.run("ds_attention_mass", load().ds_attention_mass, _at(q), _at(cache), cstep, _at(scales), sstep, dt, block, T,
-             _at(idx) if k else None, k, _at(lse), batch, heads, kv_heads, d,
-             1.0 / math.sqrt(d) if scale is None else float(scale), _at(mass), _steps(mass, 1, "mass"))
+    k = idx.shape[-1]
+    args = (_arg(q, torch.bfloat16, shape, dev, "q"), c, cstep, s, sstep, dt, block, T,
+            _arg(idx, torch.int32, (batch, k), dev, "idx") if k else None, k,
+            _arg(lse, torch.float32, (batch, heads), dev, "lse"), batch, heads, kv_heads, d,
+            d ** -0.5 if scale is None else float(scale), _rows_arg(mass, torch.float32, (batch, T), dev, "mass"),
+            _batch_step(mass, 1, "mass"))
+    _run("ds_attention_mass", load().ds_attention_mass, args, dev, stream, (q, cache, scales, idx, lse, mass))
     return mass
 
 
@@ -728,24 +727,20 @@ def ds_cache_evict(mass, budget, block=1, length=None, keep_first=0, keep_last=1
     Returns (kept int32 [batch, budget]: the blocks that stay, ascending, then -1;
     new_length int32 [batch]: the rows in them).
     """
-    torch = _torch()
-    call = _Call(_cuda_device(mass, "mass"), stream)
-    call.need(mass, torch.float32, "mass", (None, None))
-    batch, T = mass.shape
-    _dense(mass, "mass")
-    call.need(length, torch.int32, "length", (batch,), optional=True)
+    import torch
+    dev = _lead(mass, 2, "mass")
+    batch, T = shape = mass.shape
+    m = _rows_arg(mass, torch.float32, shape, dev, "mass")
     if not isinstance(budget, int) or not isinstance(block, int) or budget < 1:
         raise ValueError("budget and block must be positive ints")
-    kept = call.empty((batch, budget), torch.int32) if kept is None else call.need(kept, torch.int32, "kept", (batch, budget))
+    if kept is None:
+        kept = _new((batch, budget), torch.int32, dev, stream)
     if new_length is None:
-        new_length = call.empty((batch,), torch.int32)
-    else:
-        call.need(new_length, torch.int32, "new_length", (batch,))
-    for t, name in ((length, "length"), (kept, "kept"), (new_length, "new_length")):
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    call.run("ds_cache_evict", load().ds_cache_evict, _at(mass), _steps(mass, 1, "mass"), batch, T, _at(length), block,
-             budget, int(keep_first), int(keep_last), _at(kept), _at(new_length))
+        new_length = _new((batch,), torch.int32, dev, stream)
+    args = (m, _batch_step(mass, 1, "mass"), batch, T, _opt(length, torch.int32, (batch,), dev, "length"), block, budget,
+            int(keep_first), int(keep_last), _arg(kept, torch.int32, (batch, budget), dev, "kept"),
+            _arg(new_length, torch.int32, (batch,), dev, "new_length"))
+    _run("ds_cache_evict", load().ds_cache_evict, args, dev, stream, (mass, length, kept, new_length))
     return kept, new_length
 
 
@@ -762,35 +757,30 @@ def ds_cache_compact(kept, block=1, length=None, rows=(), blocks=(), stream=None
     shape, and its buffers do not overlap.  Rows of dst behind what stays are left
     as they were.
     """
-    torch = _torch()
-    call = _Call(_cuda_device(kept, "kept"), stream)
-    call.need(kept, torch.int32, "kept", (None, None))
+    import torch
+    dev = _lead(kept, 2, "kept")
     batch, budget = kept.shape
-    call.need(length, torch.int32, "length", (batch,), optional=True)
-    for t, name in ((kept, "kept"), (length, "length")):
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
     if not isinstance(block, int) or block < 1:
         raise ValueError("block must be a positive int")
     pairs = [(s, d, 0) for s, d in rows] + [(s, d, 1) for s, d in blocks]
     if not 1 <= len(pairs) <= DS_CACHE_MAX_ARRAYS:
         raise ValueError(f"1 to {DS_CACHE_MAX_ARRAYS} arrays can be moved")
-    call.need(pairs[0][0], None, "src")
-    T = pairs[0][0].shape[1] * (block if pairs[0][2] else 1) if pairs[0][0].dim() > 1 else 0
-    nb = (T + block - 1) // block
+    T = nb = None
     arrays = (_CacheArray * len(pairs))()
-    for a, (src, dst, per_block) in zip(arrays, pairs):
-        call.need(src, None, "src")
-        call.need(dst, src.dtype, "dst")
-        if src.dim() < 2 or src.shape[0] != batch or src.shape[1] != (nb if per_block else T):
-            raise ValueError(f"src must be [{batch}, {nb if per_block else T}, ...], got {list(src.shape)}")
-        least = budget if per_block else min(T, budget * block)
-        if dst.dim() != src.dim() or dst.shape[0] != batch or dst.shape[1] < least or dst.shape[2:] != src.shape[2:]:
-            raise ValueError(f"dst must be [{batch}, at least {least}, ...] like src, got {list(dst.shape)}")
-        _dense(src, "src"), _dense(dst, "dst")
-        size = src.element_size()
-        a.src, a.dst, a.per_block = src.data_ptr(), dst.data_ptr(), per_block
-        a.item_bytes = math.prod(src.shape[2:]) * size
-        a.src_batch_stride, a.dst_batch_stride = (src.stride(0) * size, dst.stride(0) * size) if batch > 1 else (0, 0)
-    call.run("ds_cache_compact", load().ds_cache_compact, arrays, len(pairs), _at(kept), budget, _at(length), batch, T,
-             block)
+    for i, (src, dst, per_block) in enumerate(pairs):
+        if not isinstance(src, torch.Tensor) or not isinstance(dst, torch.Tensor) or src.dim() < 2 or dst.dim() < 2:
+            raise TypeError("src and dst must be tensors [batch, items, ...]")
+        shape, to = src.shape, dst.shape
+        if T is None:
+            T = shape[1] * block if per_block else shape[1]
+            nb = (T + block - 1) // block
+        items, least, rest = (nb, budget, shape[2:]) if per_block else (T, min(T, budget * block), shape[2:])
+        if to[1] < least:
+            raise ValueError(f"dst must be [{batch}, at least {least}, ...] like src, got {list(to)}")
+        size, count = src.element_size(), math.prod(rest)
+        arrays[i] = (_rows_arg(src, src.dtype, (batch, items) + rest, dev, "src"),
+                     _rows_arg(dst, src.dtype, (batch, to[1]) + rest, dev, "dst"), src.stride(0) * size if batch > 1 else 0,
+                     dst.stride(0) * size if batch > 1 else 0, count * size, per_block)
+    args = (arrays, len(pairs), _arg(kept, torch.int32, (batch, budget), dev, "kept"), budget,
+            _opt(length, torch.int32, (batch,), dev, "length"), batch, T, block)
+    _run("ds_cache_compact", load().ds_cache_compact, args, dev, stream, (kept, length) + sum(((s, d) for s, d, _ in pairs), ()))

@@ -10,10 +10,12 @@
 // The account adds  sum_h e^(z[h, r] - lse[h])  to mass[b, r].
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "cache_format.cuh"
 #include "ptx.cuh"
+#include "tcgen05.cuh"
 
 namespace dstopk {
 
@@ -34,6 +36,7 @@ struct AqParams {
   long long scales_bstride;  // scales from one batch row's to the next
   long long mass_bstride;
   int T, k, W, B, H, Hkv, D, log_block;
+  int HT, R, log_cluster;  // attention: head tiles of a KV head, rows of a chunk, CTAs of a tile
   float scale_log2;        // scale * log2(e)
 };
 
@@ -85,70 +88,561 @@ __device__ __forceinline__ float aq_warp_max(float v) {
   return v;
 }
 
-// One CTA per batch row and query head: the scores of every slot in shared
-// memory (k + W floats), then the weighted sum column by column.
+// A warp's wait: one lane polls, so that fifteen waiting warps leave shared
+// memory to the MMAs' operand reads.
+__device__ __forceinline__ void aq_wait(uint32_t bar, uint32_t parity, const AqParams& p) {
+  if ((threadIdx.x & 31) == 0) mbar_wait_bounded(bar, parity, p.status, p.wait_ns);
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ the rows of a chunk in shared memory
+
+constexpr int kAqRows = 128;                 // rows of a chunk: M of S^T = rows . Q^T
+constexpr int kAqBlock = kAqRows * 128;      // bytes of a chunk's rows in one 64-column block
+constexpr int kAqMaxCluster = 16;
+
+// A chunk: n rows, either slots j0.. of batch row b, or its window rows j0...
+struct AqChunk {
+  int j0, n;
+  bool win;
+};
+
+// The row that place i of a chunk reads (a cache row or a window row), or -1.
+__device__ __forceinline__ int aq_chunk_row(const AqParams& p, const AqChunk& c, int b, int i) {
+  if (i >= c.n) return -1;
+  return c.win ? c.j0 + i : aq_slot(p, b, c.j0 + i);
+}
+
+// A chunk's rows are widened to bfloat16 (exactly, without their scale) and
+// stored as 64-column blocks of 128 rows x 128 bytes, 128-byte swizzle; skipped
+// rows are zeros.  Read K-major the blocks are the rows operand of the scores,
+// read MN-major that of the weighted sum.  Warp w of 8 takes rows 8 w .. + 7 and
+// 64 + 8 w .. of every block, 4 lanes to a row and 16 columns to a lane, so that
+// a row's 64 (128) bytes are one request and the two 16-byte stores of 8
+// consecutive lanes meet 8 different bank groups.  A lane loads ahead: a batch is
+// 8 pieces of 16 bytes, of codes the pieces of 4 blocks and 2 rows, of bfloat16
+// rows those of 2 blocks.
+constexpr int kAqWorkers = 8;
+
 template <int FMT>
-__global__ void __launch_bounds__(256) attn_q8_kernel(const AqParams p) {
-  extern __shared__ float z_s[];
-  __shared__ float red[9];
-  pdl_wait();
-  const int h = blockIdx.x % p.H, b = blockIdx.x / p.H, g = h / (p.H / p.Hkv);
-  const int n = p.k + aq_window(p, b), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint16_t* q = p.q + ((size_t)b * p.H + h) * p.D;
-  float m = -INFINITY;
-  for (int j = warp; j < n; j += 8) {
-    const int r = j < p.k ? aq_slot(p, b, j) : j - p.k;
-    float z = -INFINITY;
-    if (r >= 0) {
-      float dot = 0.0f;
-      if (j < p.k) {
-        const uint8_t* row = aq_row<FMT>(p, b, r, g);
-        for (int c = lane; c < p.D; c += 32) dot = fmaf(aq_bf16(q[c]), aq_value<FMT>(row, c), dot);
-        dot *= aq_scale<FMT>(p, b, r, g);
+__device__ __forceinline__ void aq_load(uint4 (&v)[8], const uint8_t* const (&src)[2], int batch, int DB) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int db = FMT == kFmtBf16 ? batch * 2 + (i >> 1) : batch * 4 + i;
+      const uint8_t* at = FMT == kFmtBf16 ? src[k] + db * 128 + (i & 1) * 16 : src[k] + db * 64;
+      v[k * 4 + i] = src[k] != nullptr && db < DB ? __ldcg(reinterpret_cast<const uint4*>(at)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+// Store the pair of blocks 2 m, 2 m + 1 from its batch.
+template <int FMT>
+__device__ __forceinline__ void aq_store(const uint4 (&v)[8], int m, int n, int DB, uint32_t rows_s) {
+  const int lane = threadIdx.x & 31, sub = (threadIdx.x >> 5) * 8 + (lane >> 2);
+  const uint32_t at0 = rows_s + (uint32_t)(m * 2 * kAqBlock + sub * 128) + (((uint32_t)(lane & 3) * 32u) ^ ((uint32_t)(sub & 7) << 4));
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    // rows from the next multiple of 16 on meet weights that no MMA reads
+    if ((int)(threadIdx.x >> 5) * 8 + k * 64 >= ((n + 15) & ~15)) break;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (2 * m + e >= DB) break;
+      uint4 lo, hi;
+      if constexpr (FMT == kFmtBf16) {
+        lo = v[k * 4 + e * 2], hi = v[k * 4 + e * 2 + 1];
       } else {
-        const uint16_t* row = p.win + (((long long)b * p.W + r) * p.Hkv + g) * p.D;
-        for (int c = lane; c < p.D; c += 32) dot = fmaf(aq_bf16(q[c]), aq_bf16(row[c]), dot);
+        const uint4 x = v[k * 4 + (m & 1) * 2 + e];
+        decode8x4<FMT>(x.x, lo.x, lo.y);
+        decode8x4<FMT>(x.y, lo.z, lo.w);
+        decode8x4<FMT>(x.z, hi.x, hi.y);
+        decode8x4<FMT>(x.w, hi.z, hi.w);
       }
-      z = aq_warp_sum(dot) * p.scale_log2;
+      const uint32_t at = at0 + (uint32_t)(e * kAqBlock + k * 64 * 128);
+      sts128(at, lo);
+      sts128(at ^ 16u, hi);
     }
-    if (lane == 0) z_s[j] = z;
-    m = fmaxf(m, z);
   }
-  const float sink = p.sink ? p.sink[h] * 1.4426950408889634f : -INFINITY;
-  if (lane == 0) red[warp] = m;
-  __syncthreads();
-  m = sink;
-  for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w]);
-  const float mu = m == -INFINITY ? 0.0f : m;
-  float l = 0.0f;
-  for (int j = threadIdx.x; j < n; j += 256) {
-    const float e = exp2f(z_s[j] - mu);
-    z_s[j] = e;
-    l += e;
+}
+
+// ------------------------------------------------------------------ attention
+//
+// A CTA owns a batch row, a KV head and N of its query heads, and every C-th
+// chunk of up to 128 attended rows; the C CTAs of a cluster share one such
+// tile.  Both products have the rows or the channels as M, so that a row's
+// scale is one factor of a thread and the queries are the narrow operand:
+//     S^T [rows, heads]    = rows . Q^T    (K = channels)
+//     O^T [channels, heads] += rows^T . P^T  (K = rows), P = 2^(z - m) * scale,
+// with S^T (N columns) and O^T (N columns for each 128 channels) in tensor
+// memory: 5 N <= 320 of its 512 columns.  The widened rows serve both products
+// (128 KiB at 512 channels), the queries stay (64 KiB), P^T takes 16 KiB.
+//
+// A chunk passes through in turn: the widened rows serve both products, so
+// nothing of the next chunk can be stored before the weighted sum has freed its
+// pair of blocks, and widening and softmax never run at the same time.  All 8
+// worker warps therefore do both: widen chunk i, block pair by block pair as it
+// is freed (the scores' MMAs follow pair by pair), issue the loads of chunk
+// i + 1, then take the softmax of chunk i, 32 rows and N/2 heads to a warp.  Warp
+// 8 issues the MMAs.  (16 workers have 96 registers to a thread, which spills;
+// with 8 the work of a thread is wide enough to cover its latencies.)
+// A head's maximum runs over lanes: a butterfly that halves the heads at each
+// step, then one exchange among the four warps of a part.  The running maximum is
+// raised, and O^T rescaled, only when a chunk exceeds it by 2^8 (P stays below
+// 2^8, and bfloat16 and float32 keep their relative precision).  A head's
+// normaliser is summed from the unrounded weights in float32, one partial sum
+// per row and thread, and reduced once at the end.
+//
+// The cluster's partial results meet in shared memory: every CTA sends each 32
+// channels x 4 heads of its O^T to the CTA that owns them, and each owner adds
+// the C contributions in rank order, scaled to the common maximum.
+constexpr int kAqThreads = (kAqWorkers + 1) * 32;
+
+template <int N>
+struct AqSmem {
+  __host__ __device__ static constexpr int q_off(int D) { return (D + 127) / 128 * 2 * kAqBlock; }
+  __host__ __device__ static constexpr int p_off(int D) { return q_off(D) + D / 64 * N * 128; }
+  __host__ __device__ static constexpr int st_off(int D) { return p_off(D) + kAqRows * 128; }  // float2 [16][N]
+  __host__ __device__ static constexpr int ft_off(int D) { return st_off(D) + kAqMaxCluster * N * 8; }  // float [16][N]
+  __host__ __device__ static constexpr int mx_off(int D) { return ft_off(D) + kAqMaxCluster * N * 4; }  // float [2][8][32]
+  __host__ __device__ static constexpr int bc_off(int D) { return mx_off(D) + 2048; }   // float [8][2][32]
+  __host__ __device__ static constexpr int bar_off(int D) { return bc_off(D) + 2048; }
+  __host__ __device__ static constexpr int slot_off(int D) { return bar_off(D) + 16 * 8; }
+  __host__ __device__ static constexpr int bytes(int D) { return slot_off(D) + 16 + 1024; }  // + alignment slack
+};
+
+// Reduce NH values, times the lane's f, over the warp's lanes; the lane's result
+// is that of value lane % NH.
+template <int NH, class Op>
+__device__ __forceinline__ float aq_reduce_heads(const float (&v)[NH], float f, Op op) {
+  const int lane = threadIdx.x & 31;
+  float t[NH / 2];
+#pragma unroll
+  for (int i = 0; i < NH / 2; ++i) {
+    const bool up = lane & (NH / 2);
+    const float send = up ? v[i] : v[i + NH / 2], keep = up ? v[i + NH / 2] : v[i];
+    t[i] = op(keep * f, __shfl_xor_sync(0xffffffffu, send * f, NH / 2));
   }
-  l = aq_warp_sum(l);
-  __syncthreads();
-  if (lane == 0) red[warp] = l;
-  __syncthreads();
-  l = exp2f(sink - mu);
-  for (int w = 0; w < 8; ++w) l += red[w];
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a NaN stays one
-  for (int c = threadIdx.x; c < p.D; c += 256) {
-    float acc = 0.0f;
-    for (int j = 0; j < n; ++j) {
-      const int r = j < p.k ? aq_slot(p, b, j) : j - p.k;
-      if (r < 0) continue;
-      const float v = j < p.k ? aq_value<FMT>(aq_row<FMT>(p, b, r, g), c) * aq_scale<FMT>(p, b, r, g)
-                              : aq_bf16(p.win[(((long long)b * p.W + r) * p.Hkv + g) * p.D + c]);
-      acc = fmaf(z_s[j], v, acc);
+#pragma unroll
+  for (int s = NH / 4; s > 0; s >>= 1) {
+#pragma unroll
+    for (int i = 0; i < s; ++i) {
+      const bool up = lane & s;
+      const float send = up ? t[i] : t[i + s], keep = up ? t[i + s] : t[i];
+      t[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, s));
     }
-    uint32_t u;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(0.0f), "f"(acc * inv));
-    p.out[((size_t)b * p.H + h) * p.D + c] = (uint16_t)u;
   }
-  if (threadIdx.x == 0 && p.lse)
-    p.lse[(size_t)b * p.H + h] = l == 0.0f ? -INFINITY : (mu + log2f(l)) * 0.6931471805599453f;
+  float r = t[0];
+#pragma unroll
+  for (int s = NH; s < 32; s <<= 1) r = op(r, __shfl_xor_sync(0xffffffffu, r, s));
+  return r;
+}
+
+// NH consecutive TMEM columns of this thread's lane.
+template <int NH>
+__device__ __forceinline__ void aq_tmem_ld(uint32_t taddr, float (&z)[NH]) {
+#pragma unroll
+  for (int i = 0; i < NH; i += 8) {
+    uint32_t r[8];
+    tmem_ld8(taddr + (uint32_t)i, r);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[i + e] = __uint_as_float(r[e]);
+  }
+}
+
+// 2^x, results below 2^-126 as 0.
+__device__ __forceinline__ float aq_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t aq_pack(float lo, float hi) {
+  uint32_t u;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
+  return u;
+}
+
+__device__ __forceinline__ void dsmem_st_f32x2(uint32_t addr, float x, float y) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
+}
+
+__device__ __forceinline__ void dsmem_st_f32x4(uint32_t addr, const float* v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3])
+               : "memory");
+}
+
+template <int FMT, int N>
+__global__ void __launch_bounds__(kAqThreads, 1)
+    attn_q8_kernel(const __grid_constant__ CUtensorMap tm_q, const AqParams p) {
+  using L_ = AqSmem<N>;
+  constexpr int NH = N / 2;  // heads of a softmax thread
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const int D = p.D, DB = D >> 6, MT = (D + 127) >> 7;
+  const uint32_t rows_s = sbase, q_s = sbase + L_::q_off(D), p_s = sbase + L_::p_off(D);
+  float2* st = reinterpret_cast<float2*>(smem + L_::st_off(D));
+  float* ft = reinterpret_cast<float*>(smem + L_::ft_off(D));
+  const uint32_t full0 = sbase + L_::bar_off(D), empty0 = full0 + 32u;  // pairs of blocks: stored [4], summed [4]
+  const uint32_t bar_q = empty0 + 32u, bar_s = bar_q + 8u, bar_p = bar_s + 8u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L_::slot_off(D));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int C = 1 << p.log_cluster, rank = blockIdx.x & (C - 1);
+  const int G = p.H / p.Hkv, tile = blockIdx.x >> p.log_cluster;
+  const int ht = tile % p.HT, g = tile / p.HT % p.Hkv, b = tile / p.HT / p.Hkv;
+  constexpr uint32_t kCols = N == 64 ? 512 : N == 32 ? 256 : 128;  // >= 5 N
+
+  if (tid == 0) {
+    for (int i = 0; i < MT; ++i) {
+      mbar_init(full0 + 8u * i, kAqWorkers);
+      mbar_init(empty0 + 8u * i, 1);
+    }
+    mbar_init(bar_q, 1);
+    mbar_init(bar_s, 1);
+    mbar_init(bar_p, kAqWorkers);
+    fence_mbar_init();
+  }
+  if (warp == kAqWorkers) {
+    tmem_alloc(smem_u32(tmem_slot), kCols);
+    tmem_relinquish();
+  }
+  // shows the cluster that this CTA runs, so that its shared memory may be written
+  if (C > 1) cluster_arrive_relaxed();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot, tmem_st = tmem + (uint32_t)(MT * N);
+  pdl_wait();
   pdl_launch_dependents();
+
+  const int wl = aq_window(p, b);
+  const int nk = (p.k + p.R - 1) / p.R, nc = nk + (wl + p.R - 1) / p.R;  // chunks of slots, and all
+  const int mine = nc > rank ? (nc - rank + C - 1) >> p.log_cluster : 0;
+  auto chunk = [&](int i) {
+    const int c = rank + (i << p.log_cluster);
+    AqChunk a;
+    a.win = c >= nk;
+    a.j0 = (a.win ? c - nk : c) * p.R;
+    a.n = min(p.R, (a.win ? wl : p.k) - a.j0);
+    return a;
+  };
+
+  if (warp < kAqWorkers) {
+    // Every address of chunk i + 1 is known while chunk i is worked on: its slots
+    // are read before chunk i is widened, its rows and scales after that.
+    const int sub = warp * 8 + (lane >> 2);  // this lane gathers rows sub and sub + 64 of a chunk
+    int r2[2] = {-1, -1};
+    const uint8_t* src[2] = {nullptr, nullptr};
+    auto slots = [&](int i) {
+      r2[0] = aq_chunk_row(p, chunk(i), b, sub);
+      r2[1] = aq_chunk_row(p, chunk(i), b, sub + 64);
+    };
+    auto place = [&](bool w) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        src[k] = r2[k] < 0 ? nullptr
+                 : w ? reinterpret_cast<const uint8_t*>(p.win + (((long long)b * p.W + r2[k]) * p.Hkv + g) * D) + (lane & 3) * 32
+                     : aq_row<FMT>(p, b, r2[k], g) + (lane & 3) * 16;
+    };
+    uint4 v[8];  // batch 0 of a chunk, loaded before the softmax of the chunk before
+    auto fetch = [&](uint4 (&x)[8], bool w, int batch) {
+      if (w)
+        aq_load<kFmtBf16>(x, src, batch, DB);
+      else
+        aq_load<FMT>(x, src, batch, DB);
+    };
+    // softmax: this thread's row and heads
+    const int part = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    float* mx = reinterpret_cast<float*>(smem + L_::mx_off(D)) + part * 4 * 32;  // maxima of the part's warps
+    float* lx = mx + 8 * 32;                                                     // and their sums
+    float* bc = reinterpret_cast<float*>(smem + L_::bc_off(D)) + warp * 64;      // this warp's broadcasts
+    float m_run = -INFINITY;  // head lane % NH of the part
+    float l[NH];
+#pragma unroll
+    for (int h = 0; h < NH; ++h) l[h] = 0.0f;
+    auto row_scale = [&](int r, bool w) { return r < 0 ? 0.0f : FMT == kFmtBf16 || w ? 1.0f : aq_scale<FMT>(p, b, r, g); };
+    int r = -1, r_next = -1;  // the slot of this thread's row, and of its row of the next chunk
+    float rs_next = 0.0f;
+    if (mine > 0) {
+      slots(0);
+      r_next = aq_chunk_row(p, chunk(0), b, row);
+      place(chunk(0).win);
+      fetch(v, chunk(0).win, 0);
+      rs_next = row_scale(r_next, chunk(0).win);
+    }
+    for (int i = 0; i < mine; ++i) {
+      const AqChunk c = chunk(i);
+      r = r_next;
+      const float rs = rs_next;
+      if (i + 1 < mine) {
+        slots(i + 1);
+        r_next = aq_chunk_row(p, chunk(i + 1), b, row);
+      }
+      // ---- widen chunk i
+      uint4 w[8];
+      fetch(w, c.win, 1);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        if (m >= MT) break;
+        if (i > 0) aq_wait(empty0 + 8u * (uint32_t)m, (uint32_t)((i - 1) & 1), p);
+        if (c.win) {
+          aq_store<kFmtBf16>((m & 1) ? w : v, m, c.n, DB, rows_s);
+          if (m < 2) aq_load<kFmtBf16>((m & 1) ? w : v, src, m + 2, DB);
+        } else {
+          aq_store<FMT>(m < 2 ? v : w, m, c.n, DB, rows_s);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full0 + 8u * (uint32_t)m);
+      }
+      // ---- the loads of chunk i + 1
+      if (i + 1 < mine) {
+        const bool w1 = chunk(i + 1).win;
+        place(w1);
+        fetch(v, w1, 0);
+        rs_next = row_scale(r_next, w1);
+      }
+      // ---- softmax of chunk i
+      const float fac = r >= 0 ? rs * p.scale_log2 : 1.0f;
+      aq_wait(bar_s, (uint32_t)(i & 1), p);
+      tc_fence_after();
+      float z[NH];
+      aq_tmem_ld<NH>(tmem_st + lane_base + (uint32_t)(part * NH), z);
+      tmem_wait_ld();
+      if (!__all_sync(0xffffffffu, r >= 0)) {
+#pragma unroll
+        for (int h = 0; h < NH; ++h) z[h] = r >= 0 ? z[h] : -INFINITY;
+      }
+      float cm = aq_reduce_heads<NH>(z, fac, [](float x, float y) { return fmaxf(x, y); });
+      if (lane < NH) mx[(warp & 3) * 32 + lane] = cm;
+      named_bar_sync(1 + part, 128);
+      const int mh = lane & (NH - 1);
+      cm = fmaxf(fmaxf(mx[mh], mx[32 + mh]), fmaxf(mx[64 + mh], mx[96 + mh]));
+      // the same data and so the same decision in the part's four warps
+      if (__any_sync(0xffffffffu, i == 0 || cm > m_run + 8.0f)) {
+        const float m_new = fmaxf(m_run, cm);
+        if (i > 0) {
+          const float f = m_new == -INFINITY ? 1.0f : exp2f(m_run - m_new);
+          __syncwarp();
+          if (lane < NH) bc[32 + lane] = f;
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < NH; ++h) l[h] *= bc[32 + h];
+          for (int m = 0; m < MT; ++m) {
+#pragma unroll
+            for (int h = 0; h < NH; h += 8) {
+              uint32_t o[8];
+              const uint32_t at = tmem + lane_base + (uint32_t)(m * N + part * NH + h);
+              tmem_ld8(at, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * bc[32 + h + e]);
+              tmem_st8(at, o);
+            }
+          }
+          tmem_wait_st();
+        }
+        m_run = m_new;
+        __syncwarp();
+        if (lane < NH) bc[lane] = m_new == -INFINITY ? 0.0f : m_new;
+        __syncwarp();
+      }
+      const uint32_t prow = p_s + (uint32_t)row * 128u, sw7 = (uint32_t)(row & 7);
+#pragma unroll
+      for (int h = 0; h < NH; h += 8) {
+        uint32_t u[4];
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const float4 mu = *reinterpret_cast<const float4*>(bc + h + e);
+          const float e0 = aq_ex2(fmaf(z[h + e], fac, -mu.x)), e1 = aq_ex2(fmaf(z[h + e + 1], fac, -mu.y));
+          const float e2 = aq_ex2(fmaf(z[h + e + 2], fac, -mu.z)), e3 = aq_ex2(fmaf(z[h + e + 3], fac, -mu.w));
+          l[h + e] += e0, l[h + e + 1] += e1, l[h + e + 2] += e2, l[h + e + 3] += e3;
+          // the weighted sum's operand: the weight times the row's scale, rounded once to bfloat16
+          u[e / 2] = aq_pack(e0 * rs, e1 * rs);
+          u[e / 2 + 1] = aq_pack(e2 * rs, e3 * rs);
+        }
+        sts128(prow + (((uint32_t)((part * NH + h) >> 3) ^ sw7) << 4), make_uint4(u[0], u[1], u[2], u[3]));
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_p);
+    }
+    // the heads' normalisers over this CTA's rows, to every CTA of the cluster
+    if (C > 1) cluster_wait();
+    const float ls = aq_reduce_heads<NH>(l, 1.0f, [](float x, float y) { return x + y; });
+    if (lane < NH) lx[(warp & 3) * 32 + lane] = ls;
+    named_bar_sync(1 + part, 128);
+    if ((warp & 3) == 0 && lane < NH) {
+      const float total = (lx[lane] + lx[32 + lane]) + (lx[64 + lane] + lx[96 + lane]);
+      const uint32_t at = smem_u32(st + rank * N + part * NH + lane);
+      if (C == 1)
+        st[part * NH + lane] = make_float2(m_run, total);
+      else
+        for (int c = 0; c < C; ++c) dsmem_st_f32x2(dsmem_map(at, (uint32_t)c), m_run, total);
+    }
+    __syncwarp();
+    if (mine > 0) {
+      aq_wait(empty0 + 8u * (uint32_t)(MT - 1), (uint32_t)((mine - 1) & 1), p);
+      tc_fence_after();
+    }
+  } else {
+    // ---------------- queries and MMAs: the warp runs as a whole, one elected lane
+    // issues, and the steps are unrolled, so that an MMA's operands are a few
+    // uniform additions (one lane on its own issues an MMA in about 120 cycles, the
+    // tensor cores take one in 52)
+    if (elect_lane()) {
+      mbar_arrive_expect_tx(bar_q, (uint32_t)(DB * N * 128));
+      tma_load_3d(q_s, &tm_q, 0, b * p.H + g * G + ht * N, 0, bar_q);
+    }
+    aq_wait(bar_q, 0, p);
+    constexpr uint32_t id1 = idesc_bf16_f32(kAqRows, N);
+    constexpr uint32_t id2 = idesc_bf16_f32(128, N) | (1u << 15) | (1u << 16);
+    const uint64_t ka = sw128_kmajor_desc(rows_s), kb = sw128_kmajor_desc(q_s);
+    const uint64_t ma = sw128_mnmajor_desc(rows_s, kAqBlock, 1024u), mb = sw128_mnmajor_desc(p_s, kAqBlock, 1024u);
+    for (int i = 0; i < mine; ++i) {
+      const int steps = (chunk(i).n + 15) >> 4;
+      for (int m = 0; m < MT; ++m) {
+        aq_wait(full0 + 8u * (uint32_t)m, (uint32_t)(i & 1), p);
+        tc_fence_after();
+        if (elect_lane()) {
+          const uint64_t a0 = desc_at(ka, (uint32_t)m * 2 * kAqBlock), b0 = desc_at(kb, (uint32_t)m * 2 * N * 128);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            if (kk < 4 || 2 * m + 1 < DB)
+              mma_bf16_ss(tmem_st, desc_at(a0, (uint32_t)((kk >> 2) * kAqBlock + (kk & 3) * 32)),
+                          desc_at(b0, (uint32_t)((kk >> 2) * N * 128 + (kk & 3) * 32)), id1, (m | kk) != 0 ? 1u : 0u);
+          if (m == MT - 1) mma_commit(bar_s);
+        }
+        __syncwarp();
+      }
+      aq_wait(bar_p, (uint32_t)(i & 1), p);
+      tc_fence_after();
+      if (elect_lane()) {
+        for (int m = 0; m < MT; ++m) {
+          const uint64_t a0 = desc_at(ma, (uint32_t)m * 2 * kAqBlock);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            if (kk < steps)
+              mma_bf16_ss(tmem + (uint32_t)(m * N), desc_at(a0, (uint32_t)(kk * 2048)), desc_at(mb, (uint32_t)(kk * 2048)), id2,
+                          (i | kk) != 0 ? 1u : 0u);
+          mma_commit(empty0 + 8u * (uint32_t)m);
+        }
+      }
+      __syncwarp();
+    }
+  }
+  __syncwarp();
+
+  // ---- the cluster's results.  The workers have waited for the last MMA:
+  // past the barrier the rows' memory is free in every CTA, and the statistics
+  // have arrived.
+  if (C > 1 && warp == kAqWorkers) cluster_wait();
+  tc_fence_before();
+  if (C > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  tc_fence_after();
+  const int q4 = warp & 3;
+  uint16_t* out = p.out + ((size_t)b * p.H + (size_t)g * G) * D;
+  const int U = (D >> 5) * (N / 4), per = (U + C - 1) >> p.log_cluster;  // pieces of 32 channels x 4 heads; per owner
+  if (warp == kAqWorkers) {
+    for (int h = lane; h < N; h += 32) {
+      const int hh = ht * N + h;
+      const float sink = p.sink && hh < G ? p.sink[g * G + hh] * 1.4426950408889634f : -INFINITY;
+      float M = sink, L = 0.0f;
+      for (int c = 0; c < C; ++c)
+        if (st[c * N + h].y != 0.0f) M = fmaxf(M, st[c * N + h].x);
+      if (sink != -INFINITY) L = exp2f(sink - M);
+      for (int c = 0; c < C; ++c) {
+        const float2 s = st[c * N + h];
+        const float f = s.y != 0.0f ? exp2f(s.x - M) : 0.0f;
+        if (s.y != 0.0f) L = fmaf(s.y, f, L);
+        ft[c * N + h] = f;
+      }
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;  // a NaN stays one
+      for (int c = 0; c < C; ++c) ft[c * N + h] *= inv;
+      if (rank == 0 && p.lse && hh < G)
+        p.lse[(size_t)b * p.H + g * G + hh] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    }
+  } else if (C > 1) {
+    for (int it = warp >> 2; it < MT * (N / 16); it += kAqWorkers / 4) {
+      const int m = it / (N / 16), c16 = it % (N / 16);
+      if (m * 128 + q4 * 32 >= D) continue;
+      float v[16];
+      if (mine > 0) {
+        aq_tmem_ld<16>(tmem + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(m * N + c16 * 16), v);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int u = (m * 4 + q4) * (N / 4) + c16 * 4 + e;
+        const uint32_t at = rows_s + (uint32_t)((rank * per + (u >> p.log_cluster)) * 512 + lane * 16);
+        dsmem_st_f32x4(dsmem_map(at, (uint32_t)(u & (C - 1))), v + 4 * e);
+      }
+    }
+  }
+  __syncwarp();
+  if (C > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  auto emit = [&](int u, const float* v) {
+    const int hg = u % (N / 4), d = u / (N / 4) * 32 + lane;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int hh = ht * N + hg * 4 + e;
+      if (hh < G) out[(size_t)hh * D + d] = (uint16_t)aq_pack(v[e], 0.0f);
+    }
+  };
+  if (C > 1 && warp < kAqWorkers) {
+    for (int s = warp; s < per; s += kAqWorkers) {
+      const int u = (s << p.log_cluster) + rank;
+      if (u >= U) break;
+      const int h = u % (N / 4) * 4;
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int c = 0; c < C; ++c) {
+        const float4 f = *reinterpret_cast<const float4*>(ft + c * N + h);
+        const uint4 x = lds128(rows_s + (uint32_t)((c * per + s) * 512 + lane * 16));
+        v[0] = fmaf(__uint_as_float(x.x), f.x, v[0]);
+        v[1] = fmaf(__uint_as_float(x.y), f.y, v[1]);
+        v[2] = fmaf(__uint_as_float(x.z), f.z, v[2]);
+        v[3] = fmaf(__uint_as_float(x.w), f.w, v[3]);
+      }
+      emit(u, v);
+    }
+  } else if (warp < kAqWorkers) {
+    for (int it = warp >> 2; it < MT * (N / 16); it += kAqWorkers / 4) {
+      const int m = it / (N / 16), c16 = it % (N / 16);
+      if (m * 128 + q4 * 32 >= D) continue;
+      float v[16];
+      if (mine > 0) {
+        aq_tmem_ld<16>(tmem + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(m * N + c16 * 16), v);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 f = *reinterpret_cast<const float4*>(ft + c16 * 16 + 4 * e);
+        v[4 * e] *= f.x, v[4 * e + 1] *= f.y, v[4 * e + 2] *= f.z, v[4 * e + 3] *= f.w;
+        emit((m * 4 + q4) * (N / 4) + c16 * 4 + e, v + 4 * e);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kAqWorkers) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
 }
 
 // One warp per batch row and slot: the row's weight, summed over the heads.

@@ -33,6 +33,63 @@ static int cache_launch(void (*kern)(P), const P& p, dim3 grid, int threads, siz
   return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? DS_OK : DS_ERR_CUDA;
 }
 
+// Queries [rows][D] bf16 in boxes of (64 channels, n heads, D/64 blocks), 128-byte swizzle.
+static bool cache_encode_q(const void* q, long long rows, int D, int n, CUtensorMap* tq) {
+  cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(D / 64)};
+  cuuint64_t str[2] = {(cuuint64_t)D * 2, 128};
+  cuuint32_t box[3] = {64, (cuuint32_t)n, (cuuint32_t)(D / 64)};
+  cuuint32_t one[3] = {1, 1, 1};
+  return g_encode(tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, str, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The attention's kernel for n = 16, 32 or 64 heads to a CTA.
+typedef void (*AqKernel)(const CUtensorMap, const AqParams);
+static AqKernel aq_kernel(int dtype, int n) {
+  if (dtype == DS_E4M3)
+    return n == 16 ? attn_q8_kernel<kFmtE4m3, 16> : n == 32 ? attn_q8_kernel<kFmtE4m3, 32> : attn_q8_kernel<kFmtE4m3, 64>;
+  return n == 16 ? attn_q8_kernel<kFmtI8, 16> : n == 32 ? attn_q8_kernel<kFmtI8, 32> : attn_q8_kernel<kFmtI8, 64>;
+}
+static int aq_smem(int n, int D) {
+  return n == 16 ? AqSmem<16>::bytes(D) : n == 32 ? AqSmem<32>::bytes(D) : AqSmem<64>::bytes(D);
+}
+
+static void aq_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int n, int D, unsigned ctas, int C) {
+  cfg->gridDim = dim3(ctas, 1, 1);
+  cfg->blockDim = dim3(kAqThreads, 1, 1);
+  cfg->dynamicSmemBytes = (size_t)aq_smem(n, D);
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 1;
+}
+
+// Once per device, from device_state: shared-memory limits, and how many
+// clusters of 1, 2, 4, 8 and 16 CTAs run at once (0: none).
+static cudaError_t cache_setup(DeviceState* s) {
+  for (int dtype : {DS_E4M3, DS_I8})
+    for (int n : {16, 32, 64}) {
+      cudaError_t e = cudaFuncSetAttribute(aq_kernel(dtype, n), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           aq_smem(n, DS_ATTN_MAX_DIM));
+      if (e != cudaSuccess) return e;
+      if (cudaFuncSetAttribute(aq_kernel(dtype, n), cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        cudaGetLastError();
+    }
+  for (int l = 0; l < 5; ++l) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    aq_config(&cfg, attr, 64, DS_ATTN_MAX_DIM, 16, 1 << l);
+    if (cudaOccupancyMaxActiveClusters(&s->aq_clusters[l], aq_kernel(DS_E4M3, 64), &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      s->aq_clusters[l] = 0;
+    }
+  }
+  return cudaSuccess;
+}
+
 // The arguments that the attention and the account share.
 static int cache_attn_check(const void* q, const void* cache, int64_t cache_batch_stride, const float* scales,
                             int64_t scales_batch_stride, int dtype, int block, int T, const int32_t* idx, int k,
@@ -131,8 +188,27 @@ extern "C" int ds_sparse_attention_q8(const void* q, const void* codes, int64_t 
   p.D = d;
   p.log_block = cache_log_block(block);
   p.scale_log2 = scale * 1.4426950408889634f;
-  return cache_launch(dtype == DS_E4M3 ? attn_q8_kernel<kFmtE4m3> : attn_q8_kernel<kFmtI8>, p,
-                      dim3((unsigned)(batch * heads)), 256, (size_t)(k + W) * 4, stream);
+  // heads of a CTA: the narrowest of 16, 32 and 64 that holds a KV head's group
+  const int G = heads / kv_heads, n = G <= 16 ? 16 : G <= 32 ? 32 : 64;
+  p.HT = (G + n - 1) / n;
+  const int64_t tiles = (int64_t)batch * kv_heads * p.HT;
+  // CTAs of a tile: doubled while all tiles' clusters run at once and a CTA keeps 32 rows or more
+  while (p.log_cluster < 4 && tiles <= s->aq_clusters[p.log_cluster + 1] && (k + W) >> (p.log_cluster + 1) >= 32)
+    ++p.log_cluster;
+  const int C = 1 << p.log_cluster;
+  if (tiles * C > INT32_MAX) return DS_ERR_ARG;
+  // rows of a chunk: as few as keep the number of chunks that a CTA passes through at what 128 rows give
+  auto turns = [&](int r) { return ((k + r - 1) / r + (W + r - 1) / r + C - 1) / C; };
+  for (p.R = kAqRows; p.R > 16 && turns(p.R - 16) == turns(kAqRows);) p.R -= 16;
+  CUtensorMap tq;
+  if (!cache_encode_q(q, (long long)batch * heads, d, n, &tq)) return DS_ERR_ARG;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  aq_config(&cfg, attr, n, d, (unsigned)(tiles * C), C);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  set_pdl(attr[1]);
+  cfg.numAttrs = pdl_on() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, aq_kernel(dtype, n), tq, p) == cudaSuccess ? DS_OK : DS_ERR_CUDA;
 }
 
 extern "C" int ds_attention_mass(const void* q, const void* cache, int64_t cache_batch_stride, const float* scales,

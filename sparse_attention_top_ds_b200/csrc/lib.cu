@@ -44,6 +44,7 @@ struct DeviceState {
   size_t sel_state_bytes = 0;
   void* attn_scratch = nullptr;  // sparse attention: per-chunk partial results, grow-only
   size_t attn_scratch_bytes = 0;
+  int aq_clusters[5] = {};  // 8-bit cache attention: clusters of 1, 2, 4, 8, 16 CTAs that run at once
 };
 
 static std::mutex g_mu;
@@ -65,6 +66,7 @@ static int take_planted_fault() {
 }
 
 static cudaError_t indexer_setup();
+static cudaError_t cache_setup(DeviceState* s);
 template <int NT>
 static cudaError_t set_stash_smem(int bytes) {
   cudaError_t e = cudaFuncSetAttribute(topk_stash_kernel<F32Keys, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -113,6 +115,7 @@ static int device_state(DeviceState** out) {
         e = cudaFuncSetAttribute(topk_cluster_kernel<BF16Keys, 512>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max);
       if (e == cudaSuccess) e = set_stash_smem<kTsThreads>(smem_max);
       if (e == cudaSuccess) e = indexer_setup();
+      if (e == cudaSuccess) e = cache_setup(&s);
       if (e != cudaSuccess) return DS_ERR_CUDA;
       g_max_cluster = topk_cluster16_ok() ? 16 : 8;
     }
