@@ -116,18 +116,16 @@ __device__ __forceinline__ int aq_chunk_row(const AqParams& p, const AqChunk& c,
 // A chunk's rows are widened to bfloat16 (exactly, without their scale) and
 // stored as 64-column blocks of 128 rows x 128 bytes, 128-byte swizzle; skipped
 // rows are zeros.  Read K-major the blocks are the rows operand of the scores,
-// read MN-major that of the weighted sum.  Warp w of 8 takes rows 8 w .. + 7 and
-// 64 + 8 w .. of every block, 4 lanes to a row and 16 columns to a lane, so that
-// a row's 64 (128) bytes are one request and the two 16-byte stores of 8
-// consecutive lanes meet 8 different bank groups.  A lane loads ahead: a batch is
-// 8 pieces of 16 bytes, of codes the pieces of 4 blocks and 2 rows, of bfloat16
-// rows those of 2 blocks.
-constexpr int kAqWorkers = 8;
-
-template <int FMT>
-__device__ __forceinline__ void aq_load(uint4 (&v)[8], const uint8_t* const (&src)[2], int batch, int DB) {
+// read MN-major that of the weighted sum.  Warp w takes rows 8 w .. + 7 of every
+// block (with K = 2, for 8 warps, 64 + 8 w .. too), 4 lanes to a row and 16
+// columns to a lane, so that a row's 64 (128) bytes are one request and the two
+// 16-byte stores of 8 consecutive lanes meet 8 different bank groups.  A lane
+// loads ahead: a batch is 4 pieces of 16 bytes of each of its K rows, of codes
+// those of 4 blocks, of bfloat16 rows those of 2 blocks.
+template <int FMT, int K>
+__device__ __forceinline__ void aq_load(uint4 (&v)[4 * K], const uint8_t* const (&src)[K], int batch, int DB) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
+  for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int db = FMT == kFmtBf16 ? batch * 2 + (i >> 1) : batch * 4 + i;
@@ -137,12 +135,12 @@ __device__ __forceinline__ void aq_load(uint4 (&v)[8], const uint8_t* const (&sr
 }
 
 // Store the pair of blocks 2 m, 2 m + 1 from its batch.
-template <int FMT>
-__device__ __forceinline__ void aq_store(const uint4 (&v)[8], int m, int n, int DB, uint32_t rows_s) {
+template <int FMT, int K>
+__device__ __forceinline__ void aq_store(const uint4 (&v)[4 * K], int m, int n, int DB, uint32_t rows_s) {
   const int lane = threadIdx.x & 31, sub = (threadIdx.x >> 5) * 8 + (lane >> 2);
   const uint32_t at0 = rows_s + (uint32_t)(m * 2 * kAqBlock + sub * 128) + (((uint32_t)(lane & 3) * 32u) ^ ((uint32_t)(sub & 7) << 4));
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
+  for (int k = 0; k < K; ++k) {
     // rows from the next multiple of 16 on meet weights that no MMA reads
     if ((int)(threadIdx.x >> 5) * 8 + k * 64 >= ((n + 15) & ~15)) break;
 #pragma unroll
@@ -195,6 +193,7 @@ __device__ __forceinline__ void aq_store(const uint4 (&v)[8], int m, int n, int 
 // The cluster's partial results meet in shared memory: every CTA sends each 32
 // channels x 4 heads of its O^T to the CTA that owns them, and each owner adds
 // the C contributions in rank order, scaled to the common maximum.
+constexpr int kAqWorkers = 8;
 constexpr int kAqThreads = (kAqWorkers + 1) * 32;
 
 template <int N>
@@ -240,12 +239,19 @@ __device__ __forceinline__ float aq_reduce_heads(const float (&v)[NH], float f, 
 // NH consecutive TMEM columns of this thread's lane.
 template <int NH>
 __device__ __forceinline__ void aq_tmem_ld(uint32_t taddr, float (&z)[NH]) {
+  if constexpr (NH == 4) {
+    uint32_t r[4];
+    tmem_ld4(taddr, r);
 #pragma unroll
-  for (int i = 0; i < NH; i += 8) {
-    uint32_t r[8];
-    tmem_ld8(taddr + (uint32_t)i, r);
+    for (int e = 0; e < 4; ++e) z[e] = __uint_as_float(r[e]);
+  } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) z[i + e] = __uint_as_float(r[e]);
+    for (int i = 0; i < NH; i += 8) {
+      uint32_t r[8];
+      tmem_ld8(taddr + (uint32_t)i, r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[i + e] = __uint_as_float(r[e]);
+    }
   }
 }
 
@@ -348,9 +354,9 @@ __global__ void __launch_bounds__(kAqThreads, 1)
     uint4 v[8];  // batch 0 of a chunk, loaded before the softmax of the chunk before
     auto fetch = [&](uint4 (&x)[8], bool w, int batch) {
       if (w)
-        aq_load<kFmtBf16>(x, src, batch, DB);
+        aq_load<kFmtBf16, 2>(x, src, batch, DB);
       else
-        aq_load<FMT>(x, src, batch, DB);
+        aq_load<FMT, 2>(x, src, batch, DB);
     };
     // softmax: this thread's row and heads
     const int part = warp >> 2, row = (warp & 3) * 32 + lane;
@@ -388,10 +394,10 @@ __global__ void __launch_bounds__(kAqThreads, 1)
         if (m >= MT) break;
         if (i > 0) aq_wait(empty0 + 8u * (uint32_t)m, (uint32_t)((i - 1) & 1), p);
         if (c.win) {
-          aq_store<kFmtBf16>((m & 1) ? w : v, m, c.n, DB, rows_s);
-          if (m < 2) aq_load<kFmtBf16>((m & 1) ? w : v, src, m + 2, DB);
+          aq_store<kFmtBf16, 2>((m & 1) ? w : v, m, c.n, DB, rows_s);
+          if (m < 2) aq_load<kFmtBf16, 2>((m & 1) ? w : v, src, m + 2, DB);
         } else {
-          aq_store<FMT>(m < 2 ? v : w, m, c.n, DB, rows_s);
+          aq_store<FMT, 2>(m < 2 ? v : w, m, c.n, DB, rows_s);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -645,29 +651,181 @@ __global__ void __launch_bounds__(kAqThreads, 1)
   }
 }
 
-// One warp per batch row and slot: the row's weight, summed over the heads.
-template <int FMT>
-__global__ void __launch_bounds__(256) attn_mass_kernel(const AqParams p) {
-  pdl_wait();
-  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (i < (long long)p.B * p.k) {
-    const int b = (int)(i / p.k), r = aq_slot(p, b, (int)(i % p.k)), G = p.H / p.Hkv;
-    if (r >= 0) {
-      float w = 0.0f;
-      for (int h = 0; h < p.H; ++h) {
-        const uint16_t* q = p.q + ((size_t)b * p.H + h) * p.D;
-        const uint8_t* row = aq_row<FMT>(p, b, r, h / G);
-        float dot = 0.0f;
-        for (int c = lane; c < p.D; c += 32) dot = fmaf(aq_bf16(q[c]), aq_value<FMT>(row, c), dot);
-        dot = aq_warp_sum(dot) * aq_scale<FMT>(p, b, r, h / G);
-        const float lse = p.lse[(size_t)b * p.H + h];
-        if (lse != -INFINITY) w += exp2f(fmaf(dot, p.scale_log2, lse * -1.4426950408889634f));
-      }
-      if (lane == 0) atomicAdd(p.mass + b * p.mass_bstride + r, w);
-    }
+// ------------------------------------------------------------------ the account
+//
+// A cluster owns a batch row and a chunk of up to 128 slots, its CTAs each a tile
+// of up to 64 query heads of one KV head (and every C-th tile after that).  The
+// scores are recomputed as above, S^T [rows, heads] = rows . Q^T: the account
+// needs the weights in float32, which the attention rounds, and reading 2 bytes
+// of a score for every head and row would cost more than the row's own bytes.
+// With a row to a thread the sum over heads never leaves the thread: four
+// threads share a row, their sums and then the CTAs' are added in a fixed order,
+// and each slot's total is added to its account once.
+constexpr int kAmWorkers = 16;
+constexpr int kAmThreads = (kAmWorkers + 1) * 32;
+constexpr int kAmMaxCluster = 8;
+
+template <int N>
+struct AmSmem {
+  __host__ __device__ static constexpr int q_off(int D) { return D / 64 * kAqBlock; }
+  __host__ __device__ static constexpr int lse_off(int D) { return q_off(D) + D / 64 * N * 128; }  // float [N]
+  __host__ __device__ static constexpr int part_off(int D) { return lse_off(D) + N * 4; }          // float [4][128]
+  __host__ __device__ static constexpr int sum_off(int D) { return part_off(D) + 2048; }           // float [8][128]
+  __host__ __device__ static constexpr int bar_off(int D) { return sum_off(D) + kAmMaxCluster * 512; }
+  __host__ __device__ static constexpr int slot_off(int D) { return bar_off(D) + 6 * 8; }
+  __host__ __device__ static constexpr int bytes(int D) { return slot_off(D) + 16 + 1024; }  // + alignment slack
+};
+
+template <int FMT, int N>
+__global__ void __launch_bounds__(kAmThreads, 1)
+    attn_mass_kernel(const __grid_constant__ CUtensorMap tm_q, const AqParams p) {
+  using L_ = AmSmem<N>;
+  constexpr int NH = N / 4;  // heads of an epilogue thread
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const int D = p.D, DB = D >> 6, MT = (D + 127) >> 7;
+  const uint32_t rows_s = sbase, q_s = sbase + L_::q_off(D);
+  float* lse_s = reinterpret_cast<float*>(smem + L_::lse_off(D));
+  float* part_s = reinterpret_cast<float*>(smem + L_::part_off(D));
+  float* sum_s = reinterpret_cast<float*>(smem + L_::sum_off(D));
+  const uint32_t full0 = sbase + L_::bar_off(D), bar_q = full0 + 32u, bar_s = bar_q + 8u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L_::slot_off(D));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int C = 1 << p.log_cluster, rank = blockIdx.x & (C - 1);
+  const int G = p.H / p.Hkv, tiles = p.Hkv * p.HT;
+  const int nk = (p.k + p.R - 1) / p.R, b = (int)(blockIdx.x >> p.log_cluster) / nk;
+  const int j0 = (int)(blockIdx.x >> p.log_cluster) % nk * p.R;
+  const AqChunk chunk = {j0, min(p.R, p.k - j0), false};
+  constexpr uint32_t kCols = N < 32 ? 32 : N;
+
+  if (tid == 0) {
+    for (int i = 0; i < MT; ++i) mbar_init(full0 + 8u * i, kAmWorkers);
+    mbar_init(bar_q, 1);
+    mbar_init(bar_s, 1);
+    fence_mbar_init();
   }
+  if (warp == kAmWorkers) {
+    tmem_alloc(smem_u32(tmem_slot), kCols);
+    tmem_relinquish();
+  }
+  if (C > 1) cluster_arrive_relaxed();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
   pdl_launch_dependents();
+
+  const int sub = warp * 8 + (lane >> 2);                     // workers: the row this lane gathers,
+  const int row = (warp & 3) * 32 + lane, part = warp >> 2;   // and the row and quarter of the heads it sums
+  const int r_load = warp < kAmWorkers ? aq_chunk_row(p, chunk, b, sub) : -1;
+  const int r = warp < kAmWorkers ? aq_chunk_row(p, chunk, b, row) : -1;
+  float total = 0.0f;
+  int turn = 0;
+  for (int t = rank, g_held = -1; t < tiles; t += C, ++turn) {
+    const int g = t / p.HT, ht = t % p.HT, heads = min(N, G - ht * N);
+    if (warp < kAmWorkers) {
+      float fac = r >= 0 ? p.scale_log2 : 0.0f;
+      if (FMT != kFmtBf16 && r >= 0) fac *= aq_scale<FMT>(p, b, r, g);
+      if (g != g_held) {
+        const uint8_t* src[1] = {r_load < 0 ? nullptr : aq_row<FMT>(p, b, r_load, g) + (lane & 3) * (FMT == kFmtBf16 ? 32 : 16)};
+        uint4 v[4], w[4];
+        aq_load<FMT, 1>(v, src, 0, DB);
+        aq_load<FMT, 1>(w, src, 1, DB);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          if (m >= MT) break;
+          if constexpr (FMT == kFmtBf16) {
+            aq_store<FMT, 1>((m & 1) ? w : v, m, chunk.n, DB, rows_s);
+            if (m < 2) aq_load<FMT, 1>((m & 1) ? w : v, src, m + 2, DB);
+          } else {
+            aq_store<FMT, 1>(m < 2 ? v : w, m, chunk.n, DB, rows_s);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full0 + 8u * (uint32_t)m);
+        }
+      } else if (lane == 0) {
+        for (int m = 0; m < MT; ++m) mbar_arrive(full0 + 8u * (uint32_t)m);  // the rows are still there
+      }
+      // log2 units; infinite where a head adds nothing
+      if (tid < N) {
+        const float l = tid < heads ? p.lse[(size_t)b * p.H + g * G + ht * N + tid] : INFINITY;
+        lse_s[tid] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
+      }
+      named_bar_sync(1, kAmWorkers * 32);
+      aq_wait(bar_s, (uint32_t)(turn & 1), p);
+      tc_fence_after();
+      float z[NH];
+      aq_tmem_ld<NH>(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(part * NH), z);
+      tmem_wait_ld();
+      float sum = 0.0f;
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        const float ls = lse_s[part * NH + h];
+        const float e = aq_ex2(fmaf(z[h], fac, -ls));
+        sum += ls == INFINITY ? 0.0f : e;
+      }
+      total += sum;
+      tc_fence_before();
+      named_bar_sync(1, kAmWorkers * 32);  // lse_s and the scores have been read
+    } else {
+      if (elect_lane()) {
+        // (the scores of the tile before have been read: the workers' barrier above precedes their arrivals)
+        mbar_arrive_expect_tx(bar_q, (uint32_t)(DB * N * 128));
+        tma_load_3d(q_s, &tm_q, 0, b * p.H + g * G + ht * N, 0, bar_q);
+      }
+      aq_wait(bar_q, (uint32_t)(turn & 1), p);
+      constexpr uint32_t id = idesc_bf16_f32(kAqRows, N);
+      const uint64_t ka = sw128_kmajor_desc(rows_s), kb = sw128_kmajor_desc(q_s);
+      for (int m = 0; m < MT; ++m) {
+        aq_wait(full0 + 8u * (uint32_t)m, (uint32_t)(turn & 1), p);
+        tc_fence_after();
+        if (elect_lane()) {
+          const uint64_t a0 = desc_at(ka, (uint32_t)m * 2 * kAqBlock), b0 = desc_at(kb, (uint32_t)m * 2 * N * 128);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            if (kk < 4 || 2 * m + 1 < DB)
+              mma_bf16_ss(tmem, desc_at(a0, (uint32_t)((kk >> 2) * kAqBlock + (kk & 3) * 32)),
+                          desc_at(b0, (uint32_t)((kk >> 2) * N * 128 + (kk & 3) * 32)), id, (m | kk) != 0 ? 1u : 0u);
+          if (m == MT - 1) mma_commit(bar_s);
+        }
+        __syncwarp();
+      }
+      aq_wait(bar_s, (uint32_t)(turn & 1), p);  // the queries' memory is free
+    }
+    g_held = g;
+  }
+
+  // ---- the row's four sums, then the CTAs', in order
+  if (warp < kAmWorkers) {
+    part_s[part * kAqRows + row] = total;
+    named_bar_sync(1, kAmWorkers * 32);
+  }
+  __syncwarp();
+  if (C > 1) cluster_wait();
+  if (tid < kAqRows) {
+    const float s = (part_s[tid] + part_s[kAqRows + tid]) + (part_s[2 * kAqRows + tid] + part_s[3 * kAqRows + tid]);
+    if (C == 1)
+      sum_s[tid] = s;
+    else
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dsmem_map(smem_u32(sum_s + rank * kAqRows + tid), 0u)), "f"(s) : "memory");
+  }
+  __syncwarp();
+  if (C > 1)
+    cluster_sync();
+  if (rank == 0 && tid < kAqRows && r >= 0) {
+    float s = sum_s[tid];
+    for (int i = 1; i < C; ++i) s += sum_s[i * kAqRows + tid];
+    atomicAdd(p.mass + b * p.mass_bstride + r, s);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kAmWorkers) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
 }
 
 }  // namespace dstopk

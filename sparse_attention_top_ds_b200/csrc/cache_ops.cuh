@@ -55,14 +55,30 @@ static int aq_smem(int n, int D) {
   return n == 16 ? AqSmem<16>::bytes(D) : n == 32 ? AqSmem<32>::bytes(D) : AqSmem<64>::bytes(D);
 }
 
+// The account's.
+static AqKernel am_kernel(int dtype, int n) {
+  if (dtype == DS_BF16)
+    return n == 16 ? attn_mass_kernel<kFmtBf16, 16> : n == 32 ? attn_mass_kernel<kFmtBf16, 32> : attn_mass_kernel<kFmtBf16, 64>;
+  if (dtype == DS_E4M3)
+    return n == 16 ? attn_mass_kernel<kFmtE4m3, 16> : n == 32 ? attn_mass_kernel<kFmtE4m3, 32> : attn_mass_kernel<kFmtE4m3, 64>;
+  return n == 16 ? attn_mass_kernel<kFmtI8, 16> : n == 32 ? attn_mass_kernel<kFmtI8, 32> : attn_mass_kernel<kFmtI8, 64>;
+}
+static int am_smem(int n, int D) {
+  return n == 16 ? AmSmem<16>::bytes(D) : n == 32 ? AmSmem<32>::bytes(D) : AmSmem<64>::bytes(D);
+}
+
+static void cache_cluster(cudaLaunchAttribute& a, int C) {
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = (unsigned)C;
+  a.val.clusterDim.y = 1;
+  a.val.clusterDim.z = 1;
+}
+
 static void aq_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int n, int D, unsigned ctas, int C) {
   cfg->gridDim = dim3(ctas, 1, 1);
   cfg->blockDim = dim3(kAqThreads, 1, 1);
   cfg->dynamicSmemBytes = (size_t)aq_smem(n, D);
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cache_cluster(attr[0], C);
   cfg->attrs = attr;
   cfg->numAttrs = 1;
 }
@@ -77,6 +93,12 @@ static cudaError_t cache_setup(DeviceState* s) {
       if (e != cudaSuccess) return e;
       if (cudaFuncSetAttribute(aq_kernel(dtype, n), cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         cudaGetLastError();
+    }
+  for (int dtype : {DS_BF16, DS_E4M3, DS_I8})
+    for (int n : {16, 32, 64}) {
+      const cudaError_t e = cudaFuncSetAttribute(am_kernel(dtype, n), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 am_smem(n, DS_ATTN_MAX_DIM));
+      if (e != cudaSuccess) return e;
     }
   for (int l = 0; l < 5; ++l) {
     cudaLaunchConfig_t cfg = {};
@@ -243,10 +265,27 @@ extern "C" int ds_attention_mass(const void* q, const void* cache, int64_t cache
   p.D = d;
   p.log_block = cache_is8(dtype) ? cache_log_block(block) : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
-  return cache_launch(dtype == DS_BF16   ? attn_mass_kernel<kFmtBf16>
-                      : dtype == DS_E4M3 ? attn_mass_kernel<kFmtE4m3>
-                                         : attn_mass_kernel<kFmtI8>,
-                      p, dim3((unsigned)(((int64_t)batch * k + 7) / 8)), 256, 0, stream);
+  const int G = heads / kv_heads, n = G <= 16 ? 16 : G <= 32 ? 32 : 64;
+  p.HT = (G + n - 1) / n;
+  // a CTA to each head tile of a chunk, up to 8
+  while (p.log_cluster < 3 && 2 << p.log_cluster <= kv_heads * p.HT) ++p.log_cluster;
+  // rows of a chunk: 128, or fewer while the chunks leave half of the SMs idle (the work of a CTA is mostly latency)
+  p.R = kAqRows;
+  while (p.R > 32 && (int64_t)batch * ((k + p.R / 2 - 1) / (p.R / 2)) << p.log_cluster <= s->num_sms) p.R /= 2;
+  const int64_t ctas = (int64_t)batch * ((k + p.R - 1) / p.R) << p.log_cluster;
+  CUtensorMap tq;
+  if (!cache_encode_q(q, (long long)batch * heads, d, n, &tq)) return DS_ERR_ARG;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+  cfg.blockDim = dim3(kAmThreads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)am_smem(n, d);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cache_cluster(attr[0], 1 << p.log_cluster);
+  set_pdl(attr[1]);
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_on() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, am_kernel(dtype, n), tq, p) == cudaSuccess ? DS_OK : DS_ERR_CUDA;
 }
 
 extern "C" int ds_cache_evict(const float* mass, int64_t mass_batch_stride, int batch, int T, const int32_t* len,
