@@ -534,7 +534,7 @@ def _rows_arg(t, dtype, shape, dev, name, lead=1):
 
 def _batch_step(t, unit, name):
     """Batch stride of t [batch, ...] in units of ``unit`` elements."""
-    st = t.stride(0) if t.shape[0] > 1 else t[0].numel()
+    st = t.stride(0) if t.shape[0] > 1 else t.numel()
     if st % unit:
         raise ValueError(f"{name}: the batch stride must be whole rows")
     return st // unit
@@ -552,15 +552,17 @@ def _lead(t, dims, name):
     return t.device
 
 
-def _new(shape, dtype, dev, stream):
-    import torch
+def _new(like, shape, dtype, stream):
+    """A new tensor on the device of ``like``, of the stream that will write it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
+    import torch
+    dev = like.device
     here = torch.cuda.current_stream(dev)
     if stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, expected {dev}")
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=dev)
+        t = like.new_empty(shape, dtype=dtype)
     if here != stream:
         t.record_stream(here)
     return t
@@ -671,9 +673,9 @@ def ds_sparse_attention_q8(q, codes, scales, idx, block, scale=None, win=None, w
         wp = _arg(win, torch.bfloat16, (batch, W, kv_heads, d), dev, "win") if W else None
     lp, sp = _opt(win_len, torch.int32, (batch,), dev, "win_len"), _opt(sink, torch.float32, (heads,), dev, "sink")
     if out is None:
-        out = _new(shape, torch.bfloat16, dev, stream)
+        out = _new(q, shape, torch.bfloat16, stream)
     if lse is None and return_lse:
-        lse = _new((batch, heads), torch.float32, dev, stream)
+        lse = _new(q, (batch, heads), torch.float32, stream)
     args = (qp, c, cstep, s, sstep, dt, block, T, ip, k, wp, W, lp, sp, batch, heads, kv_heads, d,
             d ** -0.5 if scale is None else float(scale), _arg(out, torch.bfloat16, shape, dev, "out"),
             _opt(lse, torch.float32, (batch, heads), dev, "lse"))
@@ -734,9 +736,9 @@ def ds_cache_evict(mass, budget, block=1, length=None, keep_first=0, keep_last=1
     if not isinstance(budget, int) or not isinstance(block, int) or budget < 1:
         raise ValueError("budget and block must be positive ints")
     if kept is None:
-        kept = _new((batch, budget), torch.int32, dev, stream)
+        kept = _new(mass, (batch, budget), torch.int32, stream)
     if new_length is None:
-        new_length = _new((batch,), torch.int32, dev, stream)
+        new_length = _new(mass, (batch,), torch.int32, stream)
     args = (m, _batch_step(mass, 1, "mass"), batch, T, _opt(length, torch.int32, (batch,), dev, "length"), block, budget,
             int(keep_first), int(keep_last), _arg(kept, torch.int32, (batch, budget), dev, "kept"),
             _arg(new_length, torch.int32, (batch,), dev, "new_length"))
@@ -762,25 +764,29 @@ def ds_cache_compact(kept, block=1, length=None, rows=(), blocks=(), stream=None
     batch, budget = kept.shape
     if not isinstance(block, int) or block < 1:
         raise ValueError("block must be a positive int")
-    pairs = [(s, d, 0) for s, d in rows] + [(s, d, 1) for s, d in blocks]
-    if not 1 <= len(pairs) <= DS_CACHE_MAX_ARRAYS:
+    n = len(rows) + len(blocks)
+    if not 1 <= n <= DS_CACHE_MAX_ARRAYS:
         raise ValueError(f"1 to {DS_CACHE_MAX_ARRAYS} arrays can be moved")
-    T = nb = None
-    arrays = (_CacheArray * len(pairs))()
-    for i, (src, dst, per_block) in enumerate(pairs):
-        if not isinstance(src, torch.Tensor) or not isinstance(dst, torch.Tensor) or src.dim() < 2 or dst.dim() < 2:
-            raise TypeError("src and dst must be tensors [batch, items, ...]")
-        shape, to = src.shape, dst.shape
-        if T is None:
-            T = shape[1] * block if per_block else shape[1]
-            nb = (T + block - 1) // block
-        items, least, rest = (nb, budget, shape[2:]) if per_block else (T, min(T, budget * block), shape[2:])
-        if to[1] < least:
-            raise ValueError(f"dst must be [{batch}, at least {least}, ...] like src, got {list(to)}")
-        size, count = src.element_size(), math.prod(rest)
-        arrays[i] = (_rows_arg(src, src.dtype, (batch, items) + rest, dev, "src"),
-                     _rows_arg(dst, src.dtype, (batch, to[1]) + rest, dev, "dst"), src.stride(0) * size if batch > 1 else 0,
-                     dst.stride(0) * size if batch > 1 else 0, count * size, per_block)
-    args = (arrays, len(pairs), _arg(kept, torch.int32, (batch, budget), dev, "kept"), budget,
+    first = rows[0][0] if rows else blocks[0][0]
+    if not isinstance(first, torch.Tensor) or first.dim() < 2:
+        raise TypeError("src must be a tensor [batch, items, ...]")
+    T = first.shape[1] if rows else first.shape[1] * block
+    arrays, tensors = (_CacheArray * n)(), [kept, length]
+    for i, (src, dst) in enumerate((*rows, *blocks)):
+        per_block = i >= len(rows)
+        items = (T + block - 1) // block if per_block else T
+        least = budget if per_block else min(T, budget * block)
+        if not isinstance(src, torch.Tensor) or not isinstance(dst, torch.Tensor):
+            raise TypeError("src and dst must be tensors")
+        rest, m = src.shape[2:], dst.shape[1] if dst.dim() > 1 else 0
+        if m < least:
+            raise ValueError(f"dst must be [{batch}, at least {least}, ...] like src, got {list(dst.shape)}")
+        dt, size = src.dtype, src.element_size()
+        arrays[i] = (_rows_arg(src, dt, (batch, items) + rest, dev, "src"), _rows_arg(dst, dt, (batch, m) + rest, dev, "dst"),
+                     src.stride(0) * size if batch > 1 else 0, dst.stride(0) * size if batch > 1 else 0,
+                     math.prod(rest) * size, per_block)
+        if stream is not None:
+            tensors += [src, dst]
+    args = (arrays, n, _arg(kept, torch.int32, (batch, budget), dev, "kept"), budget,
             _opt(length, torch.int32, (batch,), dev, "length"), batch, T, block)
-    _run("ds_cache_compact", load().ds_cache_compact, args, dev, stream, (kept, length) + sum(((s, d) for s, d, _ in pairs), ()))
+    _run("ds_cache_compact", load().ds_cache_compact, args, dev, stream, tensors)

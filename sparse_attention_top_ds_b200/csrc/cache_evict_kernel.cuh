@@ -24,6 +24,7 @@ struct CeParams {
   int* status;
   long long mass_bstride;
   int T, block, budget, first, last;
+  int held;                // keys that a CTA's dynamic shared memory holds
 };
 
 __device__ __forceinline__ int ce_len(const int32_t* len, int T, int b, int* status) {
@@ -32,101 +33,215 @@ __device__ __forceinline__ int ce_len(const int32_t* len, int T, int b, int* sta
   return min(max(L, 0), T);
 }
 
-// Order-preserving 32-bit key, larger first; protected blocks rank above all.
-// 0 is below every key.
-__device__ __forceinline__ uint32_t ce_key(const CeParams& p, const float* mass, int n, int nb, int L) {
-  if (n < p.first || n >= nb - p.last) return 0xffffffffu;
-  const int r0 = n * p.block, r1 = min(L, r0 + p.block);
-  double sum = 0.0;
-  for (int r = r0; r < r1; ++r) sum += (double)mass[r];
+// ------------------------------------------------------------------ what stays
+//
+// A cluster of up to 8 CTAs owns a batch row, each CTA a contiguous share of its
+// blocks.  The keys are worked out once and kept in shared memory (as many as
+// fit; those of a longer share are worked out again in each pass).  The key of
+// the last block that stays is found digit by digit, 11 + 11 + 10 bits: every CTA
+// counts its share, reads the counts of the others and finds the digit by itself,
+// so a digit costs one cluster barrier.  Then each CTA knows how many blocks stay
+// before its share, each thread how many before its own run of blocks, and the
+// list comes out in order.  The bytes (4 per row) are few: what bounds it is the
+// chain of barriers.
+constexpr int kCeThreads = 1024;
+constexpr int kCeMaxCluster = 8;
+constexpr int kCeBins = 2048;
+constexpr int kCeKeys = 48 * 1024;  // keys held per CTA
+
+// Order-preserving 32-bit key, larger first; a protected block ranks above all.
+__device__ __forceinline__ uint32_t ce_order(double sum) {
   const float v = (float)sum;
   if (v != v) return 0xfffffffeu;
   const uint32_t u = __float_as_uint(v == 0.0f ? 0.0f : v);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Sum of one value per thread over a CTA of 1024, and of the threads before this one.
-__device__ __forceinline__ int ce_scan(int v, int* warp_s, int* total) {
+__device__ __forceinline__ bool ce_protected(const CeParams& p, int n, int nb) { return n < p.first || n >= nb - p.last; }
+
+// The key of block n, by one thread.
+__device__ __forceinline__ uint32_t ce_key(const CeParams& p, const float* mass, int n, int nb, int L) {
+  if (ce_protected(p, n, nb)) return 0xffffffffu;
+  double sum = 0.0;
+  for (int r = n * p.block, r1 = min(L, r + p.block); r < r1; ++r) sum += (double)__ldcg(mass + r);
+  return ce_order(sum);
+}
+
+// Sum over the CTA's threads before this one, and over all of them.
+__device__ __forceinline__ uint64_t ce_scan(uint64_t v, uint64_t* warp_s, uint64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  uint64_t x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   __syncthreads();
   if (lane == 31) warp_s[warp] = x;
   __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < 32; ++w) {
-    const int t = warp_s[w];
-    if (w < warp) before += t;
-    all += t;
+  if (warp == 0) {
+    uint64_t w = warp_s[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    warp_s[lane] = w;
   }
-  *total = all;
-  return before + x - v;
+  __syncthreads();
+  *total = warp_s[31];
+  return (warp > 0 ? warp_s[warp - 1] : 0) + x - v;
 }
 
-// One CTA per batch row: four 8-bit radix passes for the key of the last block
-// that stays, then the list in ascending order.
-__global__ void __launch_bounds__(1024) cache_evict_kernel(const CeParams p) {
-  __shared__ int hist[256];
-  __shared__ int warp_s[32];
-  __shared__ uint32_t prefix_s;
-  __shared__ int need_s;
+__device__ __forceinline__ uint2 dsmem_ld_u32x2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(kCeThreads) cache_evict_kernel(const CeParams p) {
+  extern __shared__ uint32_t keys[];                // [min(share, kCeKeys)]
+  __shared__ uint32_t hist[2][kCeBins];             // a digit's counts; two, so that one barrier parts two digits
+  __shared__ uint64_t warp_s[32];
+  __shared__ uint32_t found[3];                     // digit of the last key, blocks to take of it, blocks that have it
+  __shared__ uint64_t counts;                       // this CTA's (blocks above the key) << 32 | (equal to it)
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int C = (int)cluster_nctarank(), rank = (int)cluster_ctarank(), b = blockIdx.x / C;
+  if (C > 1) cluster_arrive_relaxed();
+  for (int i = tid; i < kCeBins; i += kCeThreads) hist[0][i] = 0;
   pdl_wait();
-  const int b = blockIdx.x;
+  pdl_launch_dependents();
   const int L = ce_len(p.len, p.T, b, p.status), nb = (L + p.block - 1) / p.block;
   const float* mass = p.mass + b * p.mass_bstride;
   int32_t* kept = p.kept + (size_t)b * p.budget;
+  const bool all = nb <= p.budget;
+  // this CTA's blocks, and each thread's run of them
+  const int share = (nb + C - 1) / C, n0 = min(nb, rank * share), n1 = min(nb, n0 + share);
+  const int held = min(n1 - n0, p.held);
+  const int run = (n1 - n0 + kCeThreads - 1) / kCeThreads, t0 = min(n1, n0 + tid * run), t1 = min(n1, t0 + run);
+  auto key = [&](int n) { return n - n0 < held ? keys[n - n0] : ce_key(p, mass, n, nb, L); };
   uint32_t prefix = 0;
-  int need = p.budget;  // blocks to take among those that match the prefix
-  if (nb > p.budget) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (threadIdx.x < 256) hist[threadIdx.x] = 0;
-      __syncthreads();
-      for (int n = threadIdx.x; n < nb; n += 1024) {
-        const uint32_t key = ce_key(p, mass, n, nb, L);
-        if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255], 1);
+  int need = p.budget;
+  uint64_t above = 0;  // blocks that stay in the CTAs before this one: above << 32 | equal
+
+  if (!all) {
+    // the keys held: a warp reads 32 rows at a time, `span` lanes to a block, four of
+    // these at once
+    const int span = min(p.block, 32), per = 32 / span, sub = lane / span;
+    for (int i0 = (tid >> 5) * per * 4; i0 < held; i0 += kCeThreads / 32 * per * 4) {
+      double sum[4] = {0.0, 0.0, 0.0, 0.0};
+      for (int o = lane % span; o < p.block; o += span) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + u * per + sub, r = (n0 + i) * p.block + o;
+          if (i < held && r < L) sum[u] += (double)__ldcg(mass + r);
+        }
       }
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        int d = 255;
-        for (; d > 0 && hist[d] < need; --d) need -= hist[d];
-        prefix_s = prefix | ((uint32_t)d << shift);
-        need_s = need;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * per + sub;
+        for (int o = span >> 1; o > 0; o >>= 1) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
+        if (i < held && lane % span == 0) keys[i] = ce_protected(p, n0 + i, nb) ? 0xffffffffu : ce_order(sum[u]);
       }
-      __syncthreads();
-      prefix = prefix_s;
-      need = need_s;
-      __syncthreads();
     }
-  }
-  // blocks above the key stay, and the first `need` of those equal to it
-  int out = 0, equal = 0;
-  for (int n0 = 0; n0 < nb; n0 += 1024) {
-    const int n = n0 + threadIdx.x;
-    const uint32_t key = n < nb && nb > p.budget ? ce_key(p, mass, n, nb, L) : 0;
-    int total = 0;
-    const int eq = n < nb && nb > p.budget && key == prefix;
-    const int rank = equal + ce_scan(eq, warp_s, &total);
-    equal += total;
-    const int stays = n < nb && (nb <= p.budget || key > prefix || (eq && rank < need));
-    const int at = out + ce_scan(stays, warp_s, &total);
-    out += total;
-    if (stays) kept[at] = n;
     __syncthreads();
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kCeBins;
+      uint32_t* h = hist[pass & 1];
+      for (int n = n0 + tid; n < n1; n += kCeThreads) {
+        const uint32_t k = key(n);
+        if (pass == 0 || k >> (shift + (pass == 1 ? 11 : 10)) == prefix >> (shift + (pass == 1 ? 11 : 10)))
+          atomicAdd(&h[(k >> shift) & (bins - 1)], 1u);
+      }
+      if (C > 1) {
+        if (pass == 0) cluster_wait();
+        cluster_sync();
+      } else {
+        __syncthreads();
+      }
+      // two bins to a thread, the highest first
+      const int hi = bins - 1 - 2 * tid;
+      uint32_t c1 = 0, c0 = 0;
+      if (hi > 0) {
+        uint2 v[kCeMaxCluster];  // the loads of all CTAs in flight at once
+#pragma unroll
+        for (int i = 0; i < kCeMaxCluster; ++i)
+          v[i] = i >= C ? make_uint2(0u, 0u) : dsmem_ld_u32x2(dsmem_map(smem_u32(h + hi - 1), (uint32_t)i));
+#pragma unroll
+        for (int i = 0; i < kCeMaxCluster; ++i) c0 += v[i].x, c1 += v[i].y;
+      }
+      if (pass < 2)
+        for (int i = tid; i < kCeBins; i += kCeThreads) hist[(pass + 1) & 1][i] = 0;
+      uint64_t total;
+      const uint32_t before = (uint32_t)ce_scan(c1 + c0, warp_s, &total);
+      if (hi > 0 && before < (uint32_t)need && before + c1 + c0 >= (uint32_t)need) {
+        const bool first = before + c1 >= (uint32_t)need;
+        found[0] = (uint32_t)(first ? hi : hi - 1);
+        found[1] = (uint32_t)need - before - (first ? 0u : c1);
+        found[2] = first ? c1 : c0;
+      }
+      __syncthreads();
+      prefix |= found[0] << shift;
+      need = (int)found[1];
+      // every key of the digit stays: the rest of the digits need not be known.  A key
+      // at or above the prefix then is above the last one that does not stay
+      if (found[2] == found[1]) {
+        prefix -= 1;
+        need = 0;
+        break;
+      }
+    }
+  } else if (C > 1) {
+    cluster_wait();
   }
-  const int kept_n = min(nb, p.budget);
-  for (int j = kept_n + threadIdx.x; j < p.budget; j += 1024) kept[j] = -1;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    // the last block may be short: it stays exactly if it is the last of the list
-    const int tail = nb > 0 && kept[kept_n - 1] == nb - 1 ? nb * p.block - L : 0;
-    p.new_len[b] = kept_n * p.block - tail;
+
+  // ---- the list
+  uint32_t gt = 0, eq = 0;
+  if (!all)
+    for (int n = t0; n < t1; ++n) {
+      const uint32_t k = key(n);
+      gt += k > prefix;
+      eq += k == prefix;
+    }
+  else
+    gt = (uint32_t)(t1 - t0);
+  uint64_t total;
+  uint64_t mine = ce_scan((uint64_t)gt << 32 | eq, warp_s, &total);
+  if (C > 1) {
+    if (tid == 0) counts = total;
+    cluster_sync();
+    if (tid < 32) {
+      uint64_t v = 0;
+      if (lane < rank) {
+        const uint2 x = dsmem_ld_u32x2(dsmem_map(smem_u32(&counts), (uint32_t)lane));
+        v = (uint64_t)x.y << 32 | x.x;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) warp_s[0] = v;
+    }
+    __syncthreads();
+    above = warp_s[0];
   }
-  pdl_launch_dependents();
+  mine += above;
+  uint32_t ngt = (uint32_t)(mine >> 32), neq = (uint32_t)mine;
+  for (int n = t0; n < t1; ++n) {
+    const uint32_t k = all ? 1u : key(n);
+    const bool is_eq = !all && k == prefix, stays = all || k > prefix || (is_eq && neq < (uint32_t)need);
+    if (stays) kept[ngt + min(neq, (uint32_t)need)] = n;
+    // the last block may be short: its holder knows whether it stays
+    if (n == nb - 1) p.new_len[b] = min(nb, p.budget) * p.block - (stays ? nb * p.block - L : 0);
+    ngt += !is_eq && stays;
+    neq += is_eq;
+  }
+  if (rank == 0) {
+    for (int j = min(nb, p.budget) + tid; j < p.budget; j += kCeThreads) kept[j] = -1;
+    if (nb == 0 && tid == 0) p.new_len[b] = 0;
+  }
+  if (C > 1) cluster_sync();  // the counts of this CTA may still be read
 }
+
+// ------------------------------------------------------------------ moving it
 
 constexpr int kCcMaxArrays = 8;
 
@@ -136,6 +251,7 @@ struct CcArray {
   long long src_bstride, dst_bstride;  // bytes
   long long item;                      // bytes of a row, or of a block's entry
   int per_block;
+  int parts;                           // bulk copies: pieces of an entry
   int vec;                             // bytes of one access: 16, 4 or 1
 };
 
@@ -145,40 +261,173 @@ struct CcParams {
   const int32_t* len;   // [B] or null (= T)
   int* status;
   int T, block, budget, n;
+  int group;            // list entries of a turn of the small arrays
+  int n_bulk;           // the first n_bulk arrays go by bulk copies
+  int B;
+  uint64_t wait_ns;
 };
 
-template <class V>
-__device__ __forceinline__ void cc_move(uint8_t* dst, const uint8_t* src, long long bytes) {
-  const long long words = bytes / (long long)sizeof(V);
-  for (long long i = threadIdx.x; i < words; i += blockDim.x)
-    reinterpret_cast<V*>(dst)[i] = reinterpret_cast<const V*>(src)[i];
+// Where an entry comes from: its block and the block's valid rows, or -1 and 0.
+__device__ __forceinline__ int cc_entry(const CcParams& p, int b, int j, int* rows) {
+  const int L = ce_len(p.len, p.T, b, p.status), nb = (L + p.block - 1) / p.block;
+  const int n = __ldcg(p.kept + (size_t)b * p.budget + j);
+  debug_range(n >= -1 && n < nb, p.status);
+  const bool ok = n >= 0 && n < nb;
+  // as far as the block's rows are valid, and within the min(T, budget * block) rows of dst
+  *rows = ok ? min(min(p.block, L - n * p.block), p.T - j * p.block) : 0;
+  return ok ? n : -1;
 }
 
-// One CTA per kept entry: every array's bytes of one block.
-__global__ void __launch_bounds__(256) cache_compact_kernel(const CcParams p) {
-  pdl_wait();
-  const int j = blockIdx.x % p.budget, b = blockIdx.x / p.budget;
-  const int L = ce_len(p.len, p.T, b, p.status), nb = (L + p.block - 1) / p.block;
-  const int n = p.kept[(size_t)b * p.budget + j];
-  debug_range(n >= -1 && n < nb, p.status);
-  if (n >= 0 && n < nb) {
-    // as far as the block's rows are valid, and within the min(T, budget * block) rows of dst
-    const int rows = min(min(p.block, L - n * p.block), p.T - j * p.block);
-    for (int i = 0; i < p.n; ++i) {
+// One array's pieces of `entries` list entries: every `threads`-th piece of this
+// thread, 8 of them in flight.
+template <class V>
+__device__ __forceinline__ void cc_move(const CcArray& a, int b, int j0, int entries, int block, const int* from,
+                                        const int* rows, int thread, int threads) {
+  const long long unit = a.per_block ? a.item : a.item * block;
+  const uint32_t per = (uint32_t)(unit / (long long)sizeof(V)), row_pieces = (uint32_t)(a.item / (long long)sizeof(V));
+  const uint32_t pieces = per * (uint32_t)entries;
+  const V* src = reinterpret_cast<const V*>(a.src + b * a.src_bstride);
+  V* dst = reinterpret_cast<V*>(a.dst + b * a.dst_bstride) + (long long)j0 * per;
+  for (uint32_t i0 = thread; i0 < pieces; i0 += threads * 8) {
+    V v[8];
+    bool there[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const uint32_t i = i0 + u * threads, e = entries == 1 ? 0 : i / per, off = i - e * per;
+      there[u] = i < pieces && from[e] >= 0 && off < (a.per_block ? per : row_pieces * (uint32_t)rows[e]);
+      if (there[u]) v[u] = __ldcs(src + (long long)from[e] * per + off);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (there[u]) __stcs(dst + i0 + u * threads, v[u]);
+  }
+}
+
+// The arrays whose blocks are small, or no multiple of 16 bytes: p.group
+// consecutive entries of a list at a time, about 32 KiB of them to a turn of
+// `threads` threads, named barrier `bar`.
+constexpr int kCcMaxGroup = 64;
+__device__ __forceinline__ void cc_move_small(const CcParams& p, int* from, int* rows, int thread, int threads, int bar) {
+  if (p.n_bulk == p.n) return;
+  const int groups = (p.budget + p.group - 1) / p.group;
+  for (int t = blockIdx.x; t < groups * p.B; t += gridDim.x) {
+    const int b = t / groups, j0 = t % groups * p.group, entries = min(p.group, p.budget - j0);
+    named_bar_sync(bar, threads);
+    if (thread < entries) from[thread] = cc_entry(p, b, j0 + thread, rows + thread);
+    named_bar_sync(bar, threads);
+    for (int i = p.n_bulk; i < p.n; ++i) {
       const CcArray& a = p.a[i];
-      const long long unit = a.per_block ? a.item : a.item * p.block;
-      const uint8_t* src = a.src + b * a.src_bstride + n * unit;
-      uint8_t* dst = a.dst + b * a.dst_bstride + j * unit;
-      const long long bytes = a.per_block ? a.item : a.item * rows;
       if (a.vec == 16)
-        cc_move<uint4>(dst, src, bytes);
+        cc_move<uint4>(a, b, j0, entries, p.block, from, rows, thread, threads);
       else if (a.vec == 4)
-        cc_move<uint32_t>(dst, src, bytes);
+        cc_move<uint32_t>(a, b, j0, entries, p.block, from, rows, thread, threads);
       else
-        cc_move<uint8_t>(dst, src, bytes);
+        cc_move<uint8_t>(a, b, j0, entries, p.block, from, rows, thread, threads);
     }
   }
+}
+
+__global__ void __launch_bounds__(256) cache_compact_kernel(const CcParams p) {
+  __shared__ int from[kCcMaxGroup], rows[kCcMaxGroup];
+  pdl_wait();
   pdl_launch_dependents();
+  cc_move_small(p, from, rows, threadIdx.x, 256, 1);
+}
+
+// Large blocks go through shared memory by bulk copies, in pieces of up to 32 KiB:
+// a persistent CTA per SM keeps kCcAhead loads in flight ahead of the store it
+// issues, and up to two stores behind it.  The threads of warp 0 work out 32
+// pieces at a time, its first lane issues; the other warps move the small arrays
+// meanwhile.  Each byte that stays is read and written once: what bounds it is the
+// memory's copy rate.
+constexpr int kCcPiece = 32768;
+constexpr int kCcStages = 6;
+constexpr int kCcAhead = 3;
+constexpr int kCcBulkThreads = 256;
+constexpr int kCcSmem = kCcStages * kCcPiece + 128;  // + alignment slack
+
+__device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+
+__global__ void __launch_bounds__(kCcBulkThreads, 1) cache_compact_bulk_kernel(const CcParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int from[kCcMaxGroup], rows[kCcMaxGroup];
+  __shared__ uint64_t bars[kCcStages];
+  const uint32_t ring = (smem_u32(smem_raw) + 127u) & ~127u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kCcStages; ++i) mbar_init(smem_u32(bars + i), 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_launch_dependents();
+  if (warp > 0) {
+    cc_move_small(p, from, rows, threadIdx.x - 32, kCcBulkThreads - 32, 1);
+    return;
+  }
+  const long long entries = (long long)p.B * p.budget, step = gridDim.x;
+  // pieces of every bulk array, array after array, entry after entry
+  long long total = 0;
+  for (int i = 0; i < p.n_bulk; ++i) total += entries * p.a[i].parts;
+  const int mine = total > blockIdx.x ? (int)((total - blockIdx.x + step - 1) / step) : 0;
+  const uint8_t* src = nullptr;  // this lane's piece of the 32 around the load in turn, and of those around the store
+  uint8_t *dst = nullptr, *dst_held = nullptr;
+  uint32_t bytes = 0, bytes_held = 0;
+  auto look = [&](int s) {
+    src = nullptr, dst = nullptr, bytes = 0;
+    long long t = blockIdx.x + step * (s + lane);
+    if (s + lane >= mine) return;
+    int i = 0;
+    for (; t >= entries * p.a[i].parts; ++i) t -= entries * p.a[i].parts;
+    const CcArray& a = p.a[i];
+    const long long e = t / a.parts;
+    const int part = (int)(t - e * a.parts), b = (int)(e / p.budget), j = (int)(e % p.budget);
+    int nrows;
+    const int n = cc_entry(p, b, j, &nrows);
+    const long long unit = a.per_block ? a.item : a.item * p.block, off = (long long)part * kCcPiece;
+    const long long have = (a.per_block ? (n >= 0 ? a.item : 0) : a.item * nrows) - off;
+    src = a.src + b * a.src_bstride + n * unit + off;
+    dst = a.dst + b * a.dst_bstride + j * unit + off;
+    bytes = n < 0 || have <= 0 ? 0u : (uint32_t)min(have, (long long)kCcPiece);
+  };
+  bool ok = true;
+  for (int s = -kCcAhead; s < mine; ++s) {
+    const int ld = s + kCcAhead;
+    if (ld < mine) {
+      if ((ld & 31) == 0) {
+        dst_held = dst, bytes_held = bytes;  // the pieces before are still to be stored
+        look(ld);
+      }
+      const uint8_t* at = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)src, ld & 31));
+      const uint32_t n = __shfl_sync(0xffffffffu, bytes, ld & 31);
+      if (lane == 0) {
+        // the store before last of this stage has read it
+        asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kCcStages - 1 - kCcAhead) : "memory");
+        if (ok && n > 0) {
+          const uint32_t bar = smem_u32(bars + ld % kCcStages);
+          mbar_arrive_expect_tx(bar, n);
+          bulk_g2s(ring + (uint32_t)(ld % kCcStages) * kCcPiece, at, n, bar);
+        } else {
+          mbar_arrive(smem_u32(bars + ld % kCcStages));
+        }
+      }
+    }
+    if (s >= 0) {
+      // piece s is among the 32 looked up last or among those before
+      const bool old = (s >> 5) != (min(ld, mine - 1) >> 5);
+      uint8_t* at = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)(old ? dst_held : dst), s & 31));
+      const uint32_t n = __shfl_sync(0xffffffffu, old ? bytes_held : bytes, s & 31);
+      if (lane == 0) {
+        ok = mbar_wait_bounded(smem_u32(bars + s % kCcStages), (uint32_t)((s / kCcStages) & 1), p.status, p.wait_ns) && ok;
+        if (ok && n > 0) bulk_s2g(at, ring + (uint32_t)(s % kCcStages) * kCcPiece, n);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+    }
+    __syncwarp();
+  }
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 }  // namespace dstopk
