@@ -172,8 +172,26 @@ extern "C" int ds_cache_quantize(const void* rows, int64_t rows_batch_stride, in
   p.D = d;
   p.T = T;
   p.log_block = lb;
-  return cache_launch(dtype == DS_E4M3 ? cache_quantize_kernel<kFmtE4m3> : cache_quantize_kernel<kFmtI8>, p,
-                      dim3((unsigned)units), 256, 0, stream);
+  p.B = batch;
+  const int pieces = (block * d) / 8;  // of 16 bytes, in a block of one KV head
+  int nt = 32;
+  while (nt * kCqPieces < pieces) nt *= 2;
+  const int groups = nt < 256 ? 256 / nt : 1;
+  const dim3 grid((unsigned)((units + groups - 1) / groups));
+#define DS_CQ(NT)                                                                                                    \
+  case NT:                                                                                                           \
+    return cache_launch(dtype == DS_E4M3 ? cache_quantize_kernel<kFmtE4m3, NT> : cache_quantize_kernel<kFmtI8, NT>, p, \
+                        grid, NT < 256 ? 256 : NT, 0, stream);
+  switch (nt) {
+    DS_CQ(32)
+    DS_CQ(64)
+    DS_CQ(128)
+    DS_CQ(256)
+    DS_CQ(512)
+    DS_CQ(1024)
+  }
+#undef DS_CQ
+  return DS_ERR_ARG;
 }
 
 extern "C" int ds_sparse_attention_q8(const void* q, const void* codes, int64_t codes_batch_stride, const float* scales,

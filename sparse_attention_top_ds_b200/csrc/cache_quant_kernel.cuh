@@ -15,6 +15,7 @@
 
 #include "cache_format.cuh"
 #include "ptx.cuh"
+#include "tcgen05.cuh"
 
 namespace dstopk {
 
@@ -26,7 +27,7 @@ struct CqParams {
   const int32_t* len;      // [B] or null (= n)
   int* status;
   long long rows_bstride, rows_rstride, codes_bstride, scales_bstride;  // elements
-  int n, Hkv, D, T;
+  int B, n, Hkv, D, T;
   int log_block;
   int nblocks;             // blocks of n rows
 };
@@ -56,37 +57,67 @@ __device__ __forceinline__ uint2 cq_encode8(const uint4& x, float inv) {
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// One CTA per block of rows and KV head, two passes over its rows.
-template <int FMT>
-__global__ void __launch_bounds__(256) cache_quantize_kernel(const CqParams p) {
+// NT threads to a block of rows and KV head (kCqGroup / NT of these to a CTA): each
+// holds up to 8 pieces of 8 values in registers, so that a row is read once, and
+// the block's largest magnitude is one integer maximum over the group (the bits of
+// a magnitude order like its value).  NT is the smallest that holds the block.
+// Bytes bound it, 2 read and 1 written for each value, but only just: a value costs
+// about 5 instructions, so addresses are advanced, not worked out, per piece.
+constexpr int kCqPieces = 8;
+
+template <int FMT, int NT>
+__global__ void __launch_bounds__(NT < 256 ? 256 : NT, NT <= 256 ? 4 : 1024 / NT) cache_quantize_kernel(const CqParams p) {
+  constexpr int kGroups = NT < 256 ? 256 / NT : 1;
+  __shared__ uint32_t warp_max[NT < 256 ? 8 : NT / 32];
   pdl_wait();
-  const int n = blockIdx.x % p.nblocks, g = (blockIdx.x / p.nblocks) % p.Hkv, b = blockIdx.x / p.nblocks / p.Hkv;
-  int blk0 = 0;
-  const int live = cq_live(p, b, &blk0);
-  const int r0 = n << p.log_block, nr = min(1 << p.log_block, live - r0);
-  if (nr > 0) {
-    const uint16_t* src = p.rows + b * p.rows_bstride + r0 * p.rows_rstride + (long long)g * p.D;
-    const int per = p.D >> 3, pieces = nr * per;
-    uint32_t a = 0;
-    for (int i = threadIdx.x; i < pieces; i += 256) {
-      const uint4 v = *(reinterpret_cast<const uint4*>(src + (i / per) * p.rows_rstride) + i % per);
-      a = max(a, max_abs_bf16x8(v));
-    }
-    __shared__ uint32_t sa;
-    if (threadIdx.x == 0) sa = 0;
-    __syncthreads();
-    atomicMax(&sa, a);
-    __syncthreads();
-    const BlockScale s = block_scale<FMT>(sa);
-    const long long row = ((long long)blk0 << p.log_block) + r0;
-    uint8_t* dst = p.codes + b * p.codes_bstride + (row * p.Hkv + g) * p.D;
-    for (int i = threadIdx.x; i < pieces; i += 256) {
-      const uint4 v = *(reinterpret_cast<const uint4*>(src + (i / per) * p.rows_rstride) + i % per);
-      *(reinterpret_cast<uint2*>(dst + (long long)(i / per) * p.Hkv * p.D) + i % per) = cq_encode8<FMT>(v, s.inv);
-    }
-    if (threadIdx.x == 0) p.scales[b * p.scales_bstride + (long long)(blk0 + n) * p.Hkv + g] = s.scale;
-  }
   pdl_launch_dependents();
+  const int group = threadIdx.x / NT, t = threadIdx.x % NT;
+  const long long unit = (long long)blockIdx.x * kGroups + group;
+  const int n = (int)(unit % p.nblocks), g = (int)(unit / p.nblocks % p.Hkv);
+  const long long b = unit / p.nblocks / p.Hkv;
+  int blk0 = 0;
+  const int live = b < p.B ? cq_live(p, (int)b, &blk0) : 0;
+  const int r0 = n << p.log_block, nr = min(1 << p.log_block, live - r0);
+  const int per = p.D >> 3;                                // pieces of a row
+  const int pieces = nr * per;
+  // from one piece of this thread to its next, NT pieces on: `hop` on, and `wrap` more past a row's end
+  const int step_row = NT / per, step_col = NT - step_row * per, row = t / per, col0 = t - row * per;
+  const uint16_t* src = p.rows + b * p.rows_bstride + (r0 + row) * p.rows_rstride + (long long)g * p.D + col0 * 8;
+  const long long hop = step_row * p.rows_rstride + step_col * 8, wrap = p.rows_rstride - p.D;
+  uint4 v[kCqPieces];
+  uint32_t a = 0;
+  int col = col0;
+#pragma unroll
+  for (int i = 0; i < kCqPieces; ++i) {
+    v[i] = t + i * NT < pieces ? __ldcs(reinterpret_cast<const uint4*>(src)) : make_uint4(0u, 0u, 0u, 0u);
+    src += hop, col += step_col;
+    if (col >= per) col -= per, src += wrap;
+  }
+#pragma unroll
+  for (int i = 0; i < kCqPieces; ++i) a = max(a, max_abs_bf16x8(v[i]));
+  a = __reduce_max_sync(0xffffffffu, a);
+  if constexpr (NT > 32) {
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = a;
+    if constexpr (NT >= 256)
+      __syncthreads();
+    else
+      named_bar_sync(1 + group, NT);
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) a = max(a, warp_max[group * (NT / 32) + w]);
+  }
+  const BlockScale s = block_scale<FMT>(a);
+  const long long first = ((long long)blk0 << p.log_block) + r0;
+  const int width = p.Hkv * p.D;
+  uint8_t* dst = p.codes + b * p.codes_bstride + (first + row) * width + (long long)g * p.D + col0 * 8;
+  const int dhop = step_row * width + step_col * 8, dwrap = width - p.D;
+  col = col0;
+#pragma unroll
+  for (int i = 0; i < kCqPieces; ++i) {
+    if (t + i * NT < pieces) *reinterpret_cast<uint2*>(dst) = cq_encode8<FMT>(v[i], s.inv);
+    dst += dhop, col += step_col;
+    if (col >= per) col -= per, dst += dwrap;
+  }
+  if (t == 0 && nr > 0) p.scales[b * p.scales_bstride + (long long)(blk0 + n) * p.Hkv + g] = s.scale;
 }
 
 }  // namespace dstopk
