@@ -8,6 +8,7 @@ fallback implementation.
 import ctypes
 import math
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # DS_TOPK_LIB may name another build, such as libdstopk_debug.so (device range checks)
@@ -39,10 +40,8 @@ DS_CACHE_MAX_ARRAYS = 8
 _lib = None
 
 
-class _CacheArray(ctypes.Structure):
-    """ds_cache_array of the header."""
-    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("src_batch_stride", ctypes.c_int64),
-                ("dst_batch_stride", ctypes.c_int64), ("item_bytes", ctypes.c_int64), ("per_block", ctypes.c_int)]
+# ds_cache_array of the header: src, dst, their batch strides, item_bytes, per_block
+_CACHE_ARRAY = "QQqqqi4x"
 
 
 class DsError(RuntimeError):
@@ -110,7 +109,7 @@ def load():
     lib.ds_attention_mass.restype = i32
     lib.ds_cache_evict.argtypes = [vp, i64, i32, i32, i32p, i32, i32, i32, i32, i32p, i32p, vp]
     lib.ds_cache_evict.restype = i32
-    lib.ds_cache_compact.argtypes = [ctypes.POINTER(_CacheArray), i32, i32p, i32, i32p, i32, i32, i32, vp]
+    lib.ds_cache_compact.argtypes = [vp, i32, i32p, i32, i32p, i32, i32, i32, vp]
     lib.ds_cache_compact.restype = i32
     _lib = lib
     return lib
@@ -492,8 +491,8 @@ def _refuse(t, dtype, shape, dev, name):
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
@@ -504,7 +503,7 @@ def _refuse(t, dtype, shape, dev, name):
 def _arg(t, dtype, shape, dev, name):
     """Address of a contiguous tensor argument."""
     try:
-        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.shape == shape:
             return t.data_ptr()
     except AttributeError:
         pass
@@ -519,7 +518,7 @@ def _rows_arg(t, dtype, shape, dev, name, lead=1):
     """Address of an argument that is contiguous behind its first ``lead``
     dimensions (sizes of one have no stride)."""
     try:
-        if t.dtype is dtype and t.shape == shape and t.device == dev:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape:
             if not t.is_contiguous():
                 step = 1
                 for n, st in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
@@ -541,7 +540,7 @@ def _batch_step(t, unit, name):
 
 
 def _lead(t, dims, name):
-    """Device of the argument that says where a call runs."""
+    """Device (its index) of the argument that says where a call runs."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -549,7 +548,7 @@ def _lead(t, dims, name):
         raise ValueError(f"{name} must be on a CUDA device")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {list(t.shape)}")
-    return t.device
+    return t.get_device()
 
 
 def _new(like, shape, dtype, stream):
@@ -571,12 +570,12 @@ def _new(like, shape, dtype, stream):
 def _run(where, fn, args, dev, stream, tensors):
     import torch
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev.index)
-    elif stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, expected {dev}")
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, expected cuda:{dev}")
     else:
         raw = stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    if torch.cuda.current_device() == dev:
         rc = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -674,11 +673,16 @@ def ds_sparse_attention_q8(q, codes, scales, idx, block, scale=None, win=None, w
     lp, sp = _opt(win_len, torch.int32, (batch,), dev, "win_len"), _opt(sink, torch.float32, (heads,), dev, "sink")
     if out is None:
         out = _new(q, shape, torch.bfloat16, stream)
+        op = out.data_ptr()
+    else:
+        op = _arg(out, torch.bfloat16, shape, dev, "out")
     if lse is None and return_lse:
         lse = _new(q, (batch, heads), torch.float32, stream)
+        ep = lse.data_ptr()
+    else:
+        ep = _opt(lse, torch.float32, (batch, heads), dev, "lse")
     args = (qp, c, cstep, s, sstep, dt, block, T, ip, k, wp, W, lp, sp, batch, heads, kv_heads, d,
-            d ** -0.5 if scale is None else float(scale), _arg(out, torch.bfloat16, shape, dev, "out"),
-            _opt(lse, torch.float32, (batch, heads), dev, "lse"))
+            d ** -0.5 if scale is None else float(scale), op, ep)
     _run("ds_sparse_attention_q8", load().ds_sparse_attention_q8, args, dev, stream,
          (q, codes, scales, idx, win, win_len, sink, out, lse))
     return (out, lse) if return_lse else out
@@ -737,11 +741,16 @@ def ds_cache_evict(mass, budget, block=1, length=None, keep_first=0, keep_last=1
         raise ValueError("budget and block must be positive ints")
     if kept is None:
         kept = _new(mass, (batch, budget), torch.int32, stream)
+        kp = kept.data_ptr()
+    else:
+        kp = _arg(kept, torch.int32, (batch, budget), dev, "kept")
     if new_length is None:
         new_length = _new(mass, (batch,), torch.int32, stream)
+        np_ = new_length.data_ptr()
+    else:
+        np_ = _arg(new_length, torch.int32, (batch,), dev, "new_length")
     args = (m, _batch_step(mass, 1, "mass"), batch, T, _opt(length, torch.int32, (batch,), dev, "length"), block, budget,
-            int(keep_first), int(keep_last), _arg(kept, torch.int32, (batch, budget), dev, "kept"),
-            _arg(new_length, torch.int32, (batch,), dev, "new_length"))
+            int(keep_first), int(keep_last), kp, np_)
     _run("ds_cache_evict", load().ds_cache_evict, args, dev, stream, (mass, length, kept, new_length))
     return kept, new_length
 
@@ -771,22 +780,20 @@ def ds_cache_compact(kept, block=1, length=None, rows=(), blocks=(), stream=None
     if not isinstance(first, torch.Tensor) or first.dim() < 2:
         raise TypeError("src must be a tensor [batch, items, ...]")
     T = first.shape[1] if rows else first.shape[1] * block
-    arrays, tensors = (_CacheArray * n)(), [kept, length]
-    for i, (src, dst) in enumerate((*rows, *blocks)):
-        per_block = i >= len(rows)
-        items = (T + block - 1) // block if per_block else T
-        least = budget if per_block else min(T, budget * block)
-        if not isinstance(src, torch.Tensor) or not isinstance(dst, torch.Tensor):
-            raise TypeError("src and dst must be tensors")
-        rest, m = src.shape[2:], dst.shape[1] if dst.dim() > 1 else 0
-        if m < least:
-            raise ValueError(f"dst must be [{batch}, at least {least}, ...] like src, got {list(dst.shape)}")
-        dt, size = src.dtype, src.element_size()
-        arrays[i] = (_rows_arg(src, dt, (batch, items) + rest, dev, "src"), _rows_arg(dst, dt, (batch, m) + rest, dev, "dst"),
-                     src.stride(0) * size if batch > 1 else 0, dst.stride(0) * size if batch > 1 else 0,
-                     math.prod(rest) * size, per_block)
-        if stream is not None:
-            tensors += [src, dst]
+    arrays, tensors = [], [kept, length]
+    for per_block, pairs, items, least in ((0, rows, T, min(T, budget * block)), (1, blocks, (T + block - 1) // block, budget)):
+        for src, dst in pairs:
+            if not isinstance(src, torch.Tensor) or not isinstance(dst, torch.Tensor):
+                raise TypeError("src and dst must be tensors")
+            shape, dt, size = src.shape, src.dtype, src.element_size()
+            rest, to = shape[2:], dst.shape
+            if len(to) < 2 or to[1] < least:
+                raise ValueError(f"dst must be [{batch}, at least {least}, ...] like src, got {list(to)}")
+            arrays += (_rows_arg(src, dt, (batch, items) + rest, dev, "src"), _rows_arg(dst, dt, (batch, to[1]) + rest, dev, "dst"),
+                       src.stride(0) * size, dst.stride(0) * size, math.prod(rest) * size, per_block)
+            if stream is not None:
+                tensors += [src, dst]
+    arrays = struct.pack(_CACHE_ARRAY * n, *arrays)
     args = (arrays, n, _arg(kept, torch.int32, (batch, budget), dev, "kept"), budget,
             _opt(length, torch.int32, (batch,), dev, "length"), batch, T, block)
     _run("ds_cache_compact", load().ds_cache_compact, args, dev, stream, tensors)

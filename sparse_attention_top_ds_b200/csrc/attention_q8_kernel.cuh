@@ -36,32 +36,14 @@ struct AqParams {
   long long scales_bstride;  // scales from one batch row's to the next
   long long mass_bstride;
   int T, k, W, B, H, Hkv, D, log_block;
-  int HT, R, log_cluster;  // attention: head tiles of a KV head, rows of a chunk, CTAs of a tile
+  int HT, R, C;            // head tiles of a KV head, rows of a chunk, CTAs of a cluster
   float scale_log2;        // scale * log2(e)
 };
-
-// The cache row of slot j of batch row b, or -1 if the slot is skipped.
-__device__ __forceinline__ int aq_slot(const AqParams& p, int b, int j) {
-  const int r = p.idx[(size_t)b * p.k + j];
-  debug_range(r >= -1 && r < p.T, p.status);
-  return r >= 0 && r < p.T ? r : -1;
-}
 
 __device__ __forceinline__ int aq_window(const AqParams& p, int b) {
   int wl = p.win_len ? p.win_len[b] : p.W;
   debug_range(wl >= 0 && wl <= p.W, p.status);
   return min(max(wl, 0), p.W);
-}
-
-__device__ __forceinline__ float aq_bf16(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-
-// Element c of a row, without its scale.
-template <int FMT>
-__device__ __forceinline__ float aq_value(const uint8_t* row, int c) {
-  if constexpr (FMT == kFmtBf16) return aq_bf16(reinterpret_cast<const uint16_t*>(row)[c]);
-  uint32_t lo, hi;
-  decode8x4<FMT>(row[c], lo, hi);
-  return __uint_as_float(lo << 16);
 }
 
 template <int FMT>
@@ -74,18 +56,6 @@ template <int FMT>
 __device__ __forceinline__ float aq_scale(const AqParams& p, int b, int r, int g) {
   if constexpr (FMT == kFmtBf16) return 1.0f;
   return p.scales[b * p.scales_bstride + (long long)(r >> p.log_block) * p.Hkv + g];
-}
-
-__device__ __forceinline__ float aq_warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-__device__ __forceinline__ float aq_warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
 }
 
 // A warp's wait: one lane polls, so that fifteen waiting warps leave shared
@@ -107,10 +77,23 @@ struct AqChunk {
   bool win;
 };
 
-// The row that place i of a chunk reads (a cache row or a window row), or -1.
-__device__ __forceinline__ int aq_chunk_row(const AqParams& p, const AqChunk& c, int b, int i) {
-  if (i >= c.n) return -1;
-  return c.win ? c.j0 + i : aq_slot(p, b, c.j0 + i);
+// The row that place i of a chunk reads (a cache row or a window row), or -1: as
+// it is read, so that its latency passes unseen until aq_checked looks at it.
+__device__ __forceinline__ int aq_chunk_slot(const AqParams& p, const AqChunk& c, int b, int i) {
+  int r = -1;
+  if (i < c.n) {
+    r = c.j0 + i;
+    // (volatile: a plain read would be moved down to where it is used)
+    if (!c.win) asm volatile("ld.global.b32 %0, [%1];" : "=r"(r) : "l"(p.idx + (size_t)b * p.k + c.j0 + i) : "memory");
+  }
+  return r;
+}
+
+// The row, or -1 if the slot is skipped.
+__device__ __forceinline__ int aq_checked(const AqParams& p, bool win, int r) {
+  if (win) return r;
+  debug_range(r >= -1 && r < p.T, p.status);
+  return r < p.T ? max(r, -1) : -1;
 }
 
 // A chunk's rows are widened to bfloat16 (exactly, without their scale) and
@@ -120,7 +103,8 @@ __device__ __forceinline__ int aq_chunk_row(const AqParams& p, const AqChunk& c,
 // block (with K = 2, for 8 warps, 64 + 8 w .. too), 4 lanes to a row and 16
 // columns to a lane, so that a row's 64 (128) bytes are one request and the two
 // 16-byte stores of 8 consecutive lanes meet 8 different bank groups.  A lane
-// loads ahead: a batch is 4 pieces of 16 bytes of each of its K rows, of codes
+// loads ahead (channels 1 and 2 of every 4 are stored exchanged, see decode8x4): a
+// batch is 4 pieces of 16 bytes of each of its K rows, of codes
 // those of 4 blocks, of bfloat16 rows those of 2 blocks.
 template <int FMT, int K>
 __device__ __forceinline__ void aq_load(uint4 (&v)[4 * K], const uint8_t* const (&src)[K], int batch, int DB) {
@@ -148,7 +132,7 @@ __device__ __forceinline__ void aq_store(const uint4 (&v)[4 * K], int m, int n, 
       if (2 * m + e >= DB) break;
       uint4 lo, hi;
       if constexpr (FMT == kFmtBf16) {
-        lo = v[k * 4 + e * 2], hi = v[k * 4 + e * 2 + 1];
+        lo = swap_middle(v[k * 4 + e * 2]), hi = swap_middle(v[k * 4 + e * 2 + 1]);
       } else {
         const uint4 x = v[k * 4 + (m & 1) * 2 + e];
         decode8x4<FMT>(x.x, lo.x, lo.y);
@@ -161,6 +145,13 @@ __device__ __forceinline__ void aq_store(const uint4 (&v)[4 * K], int m, int n, 
       sts128(at ^ 16u, hi);
     }
   }
+}
+
+// The queries in the rows' order of channels: `bytes` of them in shared memory at
+// q, by `threads` threads.
+__device__ __forceinline__ void aq_swap_queries(uint32_t q, int bytes, int thread, int threads) {
+  for (int i = thread * 16; i < bytes; i += threads * 16) sts128(q + (uint32_t)i, swap_middle(lds128(q + (uint32_t)i)));
+  fence_proxy_async_smem();
 }
 
 // ------------------------------------------------------------------ attention
@@ -291,11 +282,11 @@ __global__ void __launch_bounds__(kAqThreads, 1)
   float2* st = reinterpret_cast<float2*>(smem + L_::st_off(D));
   float* ft = reinterpret_cast<float*>(smem + L_::ft_off(D));
   const uint32_t full0 = sbase + L_::bar_off(D), empty0 = full0 + 32u;  // pairs of blocks: stored [4], summed [4]
-  const uint32_t bar_q = empty0 + 32u, bar_s = bar_q + 8u, bar_p = bar_s + 8u;
+  const uint32_t bar_q = empty0 + 32u, bar_s = bar_q + 8u, bar_p = bar_s + 8u, bar_x = bar_p + 8u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L_::slot_off(D));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int C = 1 << p.log_cluster, rank = blockIdx.x & (C - 1);
-  const int G = p.H / p.Hkv, tile = blockIdx.x >> p.log_cluster;
+  const int C = p.C, rank = blockIdx.x % C;
+  const int G = p.H / p.Hkv, tile = blockIdx.x / C;
   const int ht = tile % p.HT, g = tile / p.HT % p.Hkv, b = tile / p.HT / p.Hkv;
   constexpr uint32_t kCols = N == 64 ? 512 : N == 32 ? 256 : 128;  // >= 5 N
 
@@ -307,6 +298,7 @@ __global__ void __launch_bounds__(kAqThreads, 1)
     mbar_init(bar_q, 1);
     mbar_init(bar_s, 1);
     mbar_init(bar_p, kAqWorkers);
+    mbar_init(bar_x, kAqWorkers);  // queries reordered
     fence_mbar_init();
   }
   if (warp == kAqWorkers) {
@@ -324,9 +316,9 @@ __global__ void __launch_bounds__(kAqThreads, 1)
 
   const int wl = aq_window(p, b);
   const int nk = (p.k + p.R - 1) / p.R, nc = nk + (wl + p.R - 1) / p.R;  // chunks of slots, and all
-  const int mine = nc > rank ? (nc - rank + C - 1) >> p.log_cluster : 0;
+  const int mine = nc > rank ? (nc - rank + C - 1) / C : 0;
   auto chunk = [&](int i) {
-    const int c = rank + (i << p.log_cluster);
+    const int c = rank + i * C;
     AqChunk a;
     a.win = c >= nk;
     a.j0 = (a.win ? c - nk : c) * p.R;
@@ -341,15 +333,17 @@ __global__ void __launch_bounds__(kAqThreads, 1)
     int r2[2] = {-1, -1};
     const uint8_t* src[2] = {nullptr, nullptr};
     auto slots = [&](int i) {
-      r2[0] = aq_chunk_row(p, chunk(i), b, sub);
-      r2[1] = aq_chunk_row(p, chunk(i), b, sub + 64);
+      r2[0] = aq_chunk_slot(p, chunk(i), b, sub);
+      r2[1] = aq_chunk_slot(p, chunk(i), b, sub + 64);
     };
     auto place = [&](bool w) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        src[k] = r2[k] < 0 ? nullptr
-                 : w ? reinterpret_cast<const uint8_t*>(p.win + (((long long)b * p.W + r2[k]) * p.Hkv + g) * D) + (lane & 3) * 32
-                     : aq_row<FMT>(p, b, r2[k], g) + (lane & 3) * 16;
+      for (int k = 0; k < 2; ++k) {
+        const int r = aq_checked(p, w, r2[k]);
+        src[k] = r < 0 ? nullptr
+                 : w ? reinterpret_cast<const uint8_t*>(p.win + (((long long)b * p.W + r) * p.Hkv + g) * D) + (lane & 3) * 32
+                     : aq_row<FMT>(p, b, r, g) + (lane & 3) * 16;
+      }
     };
     uint4 v[8];  // batch 0 of a chunk, loaded before the softmax of the chunk before
     auto fetch = [&](uint4 (&x)[8], bool w, int batch) {
@@ -368,27 +362,36 @@ __global__ void __launch_bounds__(kAqThreads, 1)
     float l[NH];
 #pragma unroll
     for (int h = 0; h < NH; ++h) l[h] = 0.0f;
-    auto row_scale = [&](int r, bool w) { return r < 0 ? 0.0f : FMT == kFmtBf16 || w ? 1.0f : aq_scale<FMT>(p, b, r, g); };
-    int r = -1, r_next = -1;  // the slot of this thread's row, and of its row of the next chunk
-    float rs_next = 0.0f;
+    // (a skipped row's scale is read from block 0 and not used: nothing waits for the load here)
+    auto row_scale = [&](int r, bool w) { return FMT == kFmtBf16 || w ? 1.0f : aq_scale<FMT>(p, b, max(r, 0), g); };
+    int r = -1, r_next = -1;  // this thread's row, and its slot of the next chunk
+    float scale_next = 1.0f;
     if (mine > 0) {
+      const bool w0 = chunk(0).win;
       slots(0);
-      r_next = aq_chunk_row(p, chunk(0), b, row);
-      place(chunk(0).win);
-      fetch(v, chunk(0).win, 0);
-      rs_next = row_scale(r_next, chunk(0).win);
+      r_next = aq_chunk_slot(p, chunk(0), b, row);
+      place(w0);
+      fetch(v, w0, 0);
+      r_next = aq_checked(p, w0, r_next);
+      scale_next = row_scale(r_next, w0);
     }
     for (int i = 0; i < mine; ++i) {
       const AqChunk c = chunk(i);
       r = r_next;
-      const float rs = rs_next;
+      const float rs = r >= 0 ? scale_next : 0.0f;
       if (i + 1 < mine) {
         slots(i + 1);
-        r_next = aq_chunk_row(p, chunk(i + 1), b, row);
+        r_next = aq_chunk_slot(p, chunk(i + 1), b, row);
       }
       // ---- widen chunk i
       uint4 w[8];
       fetch(w, c.win, 1);
+      if (i == 0) {  // while the first rows are on their way
+        aq_wait(bar_q, 0, p);
+        aq_swap_queries(q_s, DB * N * 128, tid, kAqWorkers * 32);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_x);
+      }
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         if (m >= MT) break;
@@ -408,7 +411,8 @@ __global__ void __launch_bounds__(kAqThreads, 1)
         const bool w1 = chunk(i + 1).win;
         place(w1);
         fetch(v, w1, 0);
-        rs_next = row_scale(r_next, w1);
+        r_next = aq_checked(p, w1, r_next);
+        scale_next = row_scale(r_next, w1);
       }
       // ---- softmax of chunk i
       const float fac = r >= 0 ? rs * p.scale_log2 : 1.0f;
@@ -503,7 +507,7 @@ __global__ void __launch_bounds__(kAqThreads, 1)
       mbar_arrive_expect_tx(bar_q, (uint32_t)(DB * N * 128));
       tma_load_3d(q_s, &tm_q, 0, b * p.H + g * G + ht * N, 0, bar_q);
     }
-    aq_wait(bar_q, 0, p);
+    aq_wait(mine > 0 ? bar_x : bar_q, 0, p);  // (no copy may be in flight at the end)
     constexpr uint32_t id1 = idesc_bf16_f32(kAqRows, N);
     constexpr uint32_t id2 = idesc_bf16_f32(128, N) | (1u << 15) | (1u << 16);
     const uint64_t ka = sw128_kmajor_desc(rows_s), kb = sw128_kmajor_desc(q_s);
@@ -554,7 +558,8 @@ __global__ void __launch_bounds__(kAqThreads, 1)
   tc_fence_after();
   const int q4 = warp & 3;
   uint16_t* out = p.out + ((size_t)b * p.H + (size_t)g * G) * D;
-  const int U = (D >> 5) * (N / 4), per = (U + C - 1) >> p.log_cluster;  // pieces of 32 channels x 4 heads; per owner
+  const int U = (D >> 5) * (N / 4), per = (U + C - 1) / C;  // pieces of 32 channels x 4 heads; per owner
+  const uint32_t inv_C = (65536u + (uint32_t)C - 1u) / (uint32_t)C;  // u / C = u * inv_C >> 16 for u <= 256
   if (warp == kAqWorkers) {
     for (int h = lane; h < N; h += 32) {
       const int hh = ht * N + h;
@@ -575,7 +580,10 @@ __global__ void __launch_bounds__(kAqThreads, 1)
         p.lse[(size_t)b * p.H + g * G + hh] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
     }
   } else if (C > 1) {
-    for (int it = warp >> 2; it < MT * (N / 16); it += kAqWorkers / 4) {
+    // (each CTA begins elsewhere, so that they do not all send to one owner at once)
+    const int items = MT * (N / 16), turned = items * rank / C;
+    for (int j = warp >> 2; j < items; j += kAqWorkers / 4) {
+      const int it = j + turned < items ? j + turned : j + turned - items;
       const int m = it / (N / 16), c16 = it % (N / 16);
       if (m * 128 + q4 * 32 >= D) continue;
       float v[16];
@@ -586,11 +594,17 @@ __global__ void __launch_bounds__(kAqThreads, 1)
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = 0.0f;
       }
+      const int u = (m * 4 + q4) * (N / 4) + c16 * 4;
+      int slot = (int)((uint32_t)u * inv_C >> 16), owner = u - slot * C;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int u = (m * 4 + q4) * (N / 4) + c16 * 4 + e;
-        const uint32_t at = rows_s + (uint32_t)((rank * per + (u >> p.log_cluster)) * 512 + lane * 16);
-        dsmem_st_f32x4(dsmem_map(at, (uint32_t)(u & (C - 1))), v + 4 * e);
+        const uint32_t at = rows_s + (uint32_t)((rank * per + slot) * 512 + lane * 16);
+        if (owner == rank)
+          sts128(at, make_uint4(__float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]), __float_as_uint(v[4 * e + 2]),
+                                __float_as_uint(v[4 * e + 3])));
+        else
+          dsmem_st_f32x4(dsmem_map(at, (uint32_t)owner), v + 4 * e);
+        if (++owner == C) owner = 0, ++slot;
       }
     }
   }
@@ -600,7 +614,8 @@ __global__ void __launch_bounds__(kAqThreads, 1)
   else
     __syncthreads();
   auto emit = [&](int u, const float* v) {
-    const int hg = u % (N / 4), d = u / (N / 4) * 32 + lane;
+    // lane i of a piece holds the channel stored in place i of its 32
+    const int hg = u % (N / 4), d = u / (N / 4) * 32 + (lane & 28) + ((lane & 1) << 1) + ((lane >> 1) & 1);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int hh = ht * N + hg * 4 + e;
@@ -609,10 +624,11 @@ __global__ void __launch_bounds__(kAqThreads, 1)
   };
   if (C > 1 && warp < kAqWorkers) {
     for (int s = warp; s < per; s += kAqWorkers) {
-      const int u = (s << p.log_cluster) + rank;
+      const int u = s * C + rank;
       if (u >= U) break;
       const int h = u % (N / 4) * 4;
       float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
       for (int c = 0; c < C; ++c) {
         const float4 f = *reinterpret_cast<const float4*>(ft + c * N + h);
         const uint4 x = lds128(rows_s + (uint32_t)((c * per + s) * 512 + lane * 16));
@@ -672,7 +688,7 @@ struct AmSmem {
   __host__ __device__ static constexpr int part_off(int D) { return lse_off(D) + N * 4; }          // float [4][128]
   __host__ __device__ static constexpr int sum_off(int D) { return part_off(D) + 2048; }           // float [8][128]
   __host__ __device__ static constexpr int bar_off(int D) { return sum_off(D) + kAmMaxCluster * 512; }
-  __host__ __device__ static constexpr int slot_off(int D) { return bar_off(D) + 6 * 8; }
+  __host__ __device__ static constexpr int slot_off(int D) { return bar_off(D) + 8 * 8; }
   __host__ __device__ static constexpr int bytes(int D) { return slot_off(D) + 16 + 1024; }  // + alignment slack
 };
 
@@ -689,13 +705,13 @@ __global__ void __launch_bounds__(kAmThreads, 1)
   float* lse_s = reinterpret_cast<float*>(smem + L_::lse_off(D));
   float* part_s = reinterpret_cast<float*>(smem + L_::part_off(D));
   float* sum_s = reinterpret_cast<float*>(smem + L_::sum_off(D));
-  const uint32_t full0 = sbase + L_::bar_off(D), bar_q = full0 + 32u, bar_s = bar_q + 8u;
+  const uint32_t full0 = sbase + L_::bar_off(D), bar_q = full0 + 32u, bar_s = bar_q + 8u, bar_x = bar_s + 8u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L_::slot_off(D));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int C = 1 << p.log_cluster, rank = blockIdx.x & (C - 1);
+  const int C = p.C, rank = blockIdx.x % C;
   const int G = p.H / p.Hkv, tiles = p.Hkv * p.HT;
-  const int nk = (p.k + p.R - 1) / p.R, b = (int)(blockIdx.x >> p.log_cluster) / nk;
-  const int j0 = (int)(blockIdx.x >> p.log_cluster) % nk * p.R;
+  const int nk = (p.k + p.R - 1) / p.R, b = (int)blockIdx.x / C / nk;
+  const int j0 = (int)blockIdx.x / C % nk * p.R;
   const AqChunk chunk = {j0, min(p.R, p.k - j0), false};
   constexpr uint32_t kCols = N < 32 ? 32 : N;
 
@@ -703,6 +719,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
     for (int i = 0; i < MT; ++i) mbar_init(full0 + 8u * i, kAmWorkers);
     mbar_init(bar_q, 1);
     mbar_init(bar_s, 1);
+    mbar_init(bar_x, kAmWorkers);  // queries reordered
     fence_mbar_init();
   }
   if (warp == kAmWorkers) {
@@ -719,20 +736,29 @@ __global__ void __launch_bounds__(kAmThreads, 1)
 
   const int sub = warp * 8 + (lane >> 2);                     // workers: the row this lane gathers,
   const int row = (warp & 3) * 32 + lane, part = warp >> 2;   // and the row and quarter of the heads it sums
-  const int r_load = warp < kAmWorkers ? aq_chunk_row(p, chunk, b, sub) : -1;
-  const int r = warp < kAmWorkers ? aq_chunk_row(p, chunk, b, row) : -1;
+  int r_load = warp < kAmWorkers ? aq_chunk_slot(p, chunk, b, sub) : -1;
+  int r = warp < kAmWorkers ? aq_chunk_slot(p, chunk, b, row) : -1;
+  r_load = aq_checked(p, false, r_load);
+  r = aq_checked(p, false, r);
   float total = 0.0f;
   int turn = 0;
   for (int t = rank, g_held = -1; t < tiles; t += C, ++turn) {
     const int g = t / p.HT, ht = t % p.HT, heads = min(N, G - ht * N);
     if (warp < kAmWorkers) {
-      float fac = r >= 0 ? p.scale_log2 : 0.0f;
+      float fac = r >= 0 ? p.scale_log2 : 0.0f;  // (the scale's load is on its way while the rows are)
       if (FMT != kFmtBf16 && r >= 0) fac *= aq_scale<FMT>(p, b, r, g);
+      auto swap_queries = [&]() {
+        aq_wait(bar_q, (uint32_t)(turn & 1), p);
+        aq_swap_queries(q_s, DB * N * 128, tid, kAmWorkers * 32);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_x);
+      };
       if (g != g_held) {
         const uint8_t* src[1] = {r_load < 0 ? nullptr : aq_row<FMT>(p, b, r_load, g) + (lane & 3) * (FMT == kFmtBf16 ? 32 : 16)};
         uint4 v[4], w[4];
         aq_load<FMT, 1>(v, src, 0, DB);
         aq_load<FMT, 1>(w, src, 1, DB);
+        swap_queries();
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           if (m >= MT) break;
@@ -746,8 +772,10 @@ __global__ void __launch_bounds__(kAmThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(full0 + 8u * (uint32_t)m);
         }
-      } else if (lane == 0) {
-        for (int m = 0; m < MT; ++m) mbar_arrive(full0 + 8u * (uint32_t)m);  // the rows are still there
+      } else {
+        swap_queries();
+        if (lane == 0)
+          for (int m = 0; m < MT; ++m) mbar_arrive(full0 + 8u * (uint32_t)m);  // the rows are still there
       }
       // log2 units; infinite where a head adds nothing
       if (tid < N) {
@@ -776,7 +804,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
         mbar_arrive_expect_tx(bar_q, (uint32_t)(DB * N * 128));
         tma_load_3d(q_s, &tm_q, 0, b * p.H + g * G + ht * N, 0, bar_q);
       }
-      aq_wait(bar_q, (uint32_t)(turn & 1), p);
+      aq_wait(bar_x, (uint32_t)(turn & 1), p);
       constexpr uint32_t id = idesc_bf16_f32(kAqRows, N);
       const uint64_t ka = sw128_kmajor_desc(rows_s), kb = sw128_kmajor_desc(q_s);
       for (int m = 0; m < MT; ++m) {

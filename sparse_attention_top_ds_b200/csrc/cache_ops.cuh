@@ -84,7 +84,7 @@ static void aq_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int n,
 }
 
 // Once per device, from device_state: shared-memory limits, and how many
-// clusters of 1, 2, 4, 8 and 16 CTAs run at once (0: none).
+// clusters of each size of the attention run at once (0: none).
 static cudaError_t cache_setup(DeviceState* s) {
   for (int dtype : {DS_E4M3, DS_I8})
     for (int n : {16, 32, 64}) {
@@ -104,13 +104,13 @@ static cudaError_t cache_setup(DeviceState* s) {
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(cache_compact_bulk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCcSmem);
   if (e != cudaSuccess) return e;
-  for (int l = 0; l < 5; ++l) {
+  for (int c = 1; c <= kAqMaxCluster; ++c) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    aq_config(&cfg, attr, 64, DS_ATTN_MAX_DIM, 16, 1 << l);
-    if (cudaOccupancyMaxActiveClusters(&s->aq_clusters[l], aq_kernel(DS_E4M3, 64), &cfg) != cudaSuccess) {
+    aq_config(&cfg, attr, 64, DS_ATTN_MAX_DIM, (unsigned)c, c);
+    if (cudaOccupancyMaxActiveClusters(&s->aq_clusters[c], aq_kernel(DS_E4M3, 64), &cfg) != cudaSuccess) {
       cudaGetLastError();
-      s->aq_clusters[l] = 0;
+      s->aq_clusters[c] = 0;
     }
   }
   return cudaSuccess;
@@ -232,18 +232,38 @@ extern "C" int ds_sparse_attention_q8(const void* q, const void* codes, int64_t 
   p.D = d;
   p.log_block = cache_log_block(block);
   p.scale_log2 = scale * 1.4426950408889634f;
-  // heads of a CTA: the narrowest of 16, 32 and 64 that holds a KV head's group
-  const int G = heads / kv_heads, n = G <= 16 ? 16 : G <= 32 ? 32 : 64;
+  // Heads of a CTA, CTAs of a tile (while all tiles' clusters run at once) and rows
+  // of a chunk.  Measured at 512 channels, a CTA's turn of a chunk takes 3.6, 4.0 and
+  // 4.7 us with 16, 32 and 64 heads (the MMAs cost the same up to 64), the parts of a
+  // call beside its turns 5, 5 and 9 us, and 7.7, 8.7 and 13.6 where a cluster
+  // exchanges partial results; what has the least of both, over all waves of CTAs, is
+  // taken.  128 heads over 1024 + 128 rows: one batch row 16 heads, 9 CTAs 11.4 us
+  // (64, 9: 18.3), eight 32, 4 20.4 us (64, 6: 23.0), thirty-two 64, 2 37.2 us (32, 1:
+  // 40.4).
+  const int G = heads / kv_heads;
+  auto turns = [&](int r, int c) { return ((k + r - 1) / r + (W + r - 1) / r + c - 1) / c; };
+  int n = 0;
+  double best = 0.0;
+  int64_t tiles = 0;
+  static const struct {
+    int n;
+    double turn, alone, cluster;
+  } kCost[] = {{16, 3.6, 5.0, 7.7}, {32, 4.0, 5.0, 8.7}, {64, 4.7, 9.0, 13.6}};
+  for (const auto& w : kCost) {
+    const int64_t t = (int64_t)batch * kv_heads * ((G + w.n - 1) / w.n);
+    for (int c = 1; c <= kAqMaxCluster; ++c) {
+      if (c > 1 && (t > s->aq_clusters[c] || turns(kAqRows, c) == turns(kAqRows, c - 1))) continue;
+      const double waves = (double)((t * c + s->num_sms - 1) / s->num_sms);
+      const double us = waves * turns(kAqRows, c) * w.turn + (c > 1 ? w.cluster : w.alone);
+      if (n == 0 || us < best) n = w.n, best = us, tiles = t, p.C = c;
+    }
+    if (w.n >= G) break;
+  }
   p.HT = (G + n - 1) / n;
-  const int64_t tiles = (int64_t)batch * kv_heads * p.HT;
-  // CTAs of a tile: doubled while all tiles' clusters run at once and a CTA keeps 32 rows or more
-  while (p.log_cluster < 4 && tiles <= s->aq_clusters[p.log_cluster + 1] && (k + W) >> (p.log_cluster + 1) >= 32)
-    ++p.log_cluster;
-  const int C = 1 << p.log_cluster;
+  const int C = p.C;
   if (tiles * C > INT32_MAX) return DS_ERR_ARG;
-  // rows of a chunk: as few as keep the number of chunks that a CTA passes through at what 128 rows give
-  auto turns = [&](int r) { return ((k + r - 1) / r + (W + r - 1) / r + C - 1) / C; };
-  for (p.R = kAqRows; p.R > 16 && turns(p.R - 16) == turns(kAqRows);) p.R -= 16;
+  // the fewest rows that keep the number of turns
+  for (p.R = kAqRows; p.R > 16 && turns(p.R - 16, C) == turns(kAqRows, C);) p.R -= 16;
   CUtensorMap tq;
   if (!cache_encode_q(q, (long long)batch * heads, d, n, &tq)) return DS_ERR_ARG;
   cudaLaunchConfig_t cfg = {};
@@ -290,11 +310,11 @@ extern "C" int ds_attention_mass(const void* q, const void* cache, int64_t cache
   const int G = heads / kv_heads, n = G <= 16 ? 16 : G <= 32 ? 32 : 64;
   p.HT = (G + n - 1) / n;
   // a CTA to each head tile of a chunk, up to 8
-  while (p.log_cluster < 3 && 2 << p.log_cluster <= kv_heads * p.HT) ++p.log_cluster;
+  p.C = std::min(kAmMaxCluster, kv_heads * p.HT);
   // rows of a chunk: 128, or fewer while the chunks leave half of the SMs idle (the work of a CTA is mostly latency)
   p.R = kAqRows;
-  while (p.R > 32 && (int64_t)batch * ((k + p.R / 2 - 1) / (p.R / 2)) << p.log_cluster <= s->num_sms) p.R /= 2;
-  const int64_t ctas = (int64_t)batch * ((k + p.R - 1) / p.R) << p.log_cluster;
+  while (p.R > 32 && (int64_t)batch * ((k + p.R / 2 - 1) / (p.R / 2)) * p.C <= s->num_sms) p.R /= 2;
+  const int64_t ctas = (int64_t)batch * ((k + p.R - 1) / p.R) * p.C;
   CUtensorMap tq;
   if (!cache_encode_q(q, (long long)batch * heads, d, n, &tq)) return DS_ERR_ARG;
   cudaLaunchConfig_t cfg = {};
@@ -303,7 +323,7 @@ extern "C" int ds_attention_mass(const void* q, const void* cache, int64_t cache
   cfg.blockDim = dim3(kAmThreads, 1, 1);
   cfg.dynamicSmemBytes = (size_t)am_smem(n, d);
   cfg.stream = static_cast<cudaStream_t>(stream);
-  cache_cluster(attr[0], 1 << p.log_cluster);
+  cache_cluster(attr[0], p.C);
   set_pdl(attr[1]);
   cfg.attrs = attr;
   cfg.numAttrs = pdl_on() ? 2 : 1;

@@ -44,7 +44,7 @@ struct DeviceState {
   size_t sel_state_bytes = 0;
   void* attn_scratch = nullptr;  // sparse attention: per-chunk partial results, grow-only
   size_t attn_scratch_bytes = 0;
-  int aq_clusters[5] = {};  // 8-bit cache attention: clusters of 1, 2, 4, 8, 16 CTAs that run at once
+  int aq_clusters[17] = {};  // 8-bit cache attention: clusters of 1 .. 16 CTAs that run at once
 };
 
 static std::mutex g_mu;

@@ -2,6 +2,7 @@
 Python front end refuses tensors that are not on a GPU (CPU only)."""
 
 import ctypes
+import struct
 
 import pytest
 import torch
@@ -78,9 +79,7 @@ def test_compact_arguments(lib):
     def call(n=1, kept=A, budget=4, length=None, batch=2, T=100, block=16, arrays=True, **a):
         f = dict(src=0x100000, dst=0x900000, src_batch_stride=102400, dst_batch_stride=65536, item_bytes=1024, per_block=0)
         f.update(a)
-        arr = (_native._CacheArray * max(1, min(n, 9)))()
-        for i in range(len(arr)):
-            arr[i] = _native._CacheArray(**f)
+        arr = struct.pack(_native._CACHE_ARRAY, *(f[i] or 0 for i in f)) * max(1, min(n, 9))
         return lib.ds_cache_compact(arr if arrays else None, n, kept, budget, length, batch, T, block, None)
 
     for bad in (dict(arrays=False), dict(n=0), dict(n=9), dict(kept=None), dict(budget=0), dict(budget=8), dict(batch=0),
