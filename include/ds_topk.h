@@ -373,8 +373,9 @@ int ds_sparse_attention(const void* q, const void* kv, int64_t kv_batch_stride, 
  *          was (libdstopk_debug.so records DS_ERR_RANGE).
  * len      device int32 [batch] or NULL (= n): the first
  *          min(max(len[b], 0), n, T - pos[b]) rows are written; everything else
- *          in codes and scales is left as it was.  A last block that is not
- *          full has the scale of the rows given.
+ *          in codes and scales is left as it was (libdstopk_debug.so records
+ *          DS_ERR_RANGE where rows are cut).  A last block that is not full has
+ *          the scale of the rows written.
  * codes    device: batch row b's cache starts codes_batch_stride * b rows after
  *          codes; >= T if batch > 1.
  * scales   device float32: batch row b's scales start scales_batch_stride * b

@@ -483,9 +483,29 @@ def ds_compress_fold(rows, gate, out=None, stream=None):
 # recorded there, so that freeing a tensor does not hand out its memory early;
 # the caller orders the two streams, as for any other work.
 #
-# A decode step makes several of these calls per layer, so the usual call (the
-# current stream, contiguous tensors) passes each check in one comparison; the
-# reason for a refusal is worked out only once there is one.
+# A decode step makes several of these calls per layer, and the smallest run for a
+# few microseconds.  The usual call (the current stream and device, contiguous
+# tensors) is therefore marshalled by the extension _front, which returns None for
+# any other; that is marshalled here, each check in one comparison, and the reason
+# for a refusal is worked out only once there is one.
+
+_front = None
+
+
+def _load_front():
+    """Import the extension once and give it the library's addresses."""
+    global _front
+    lib = load()
+    try:
+        from . import _front as front
+    except ImportError as e:
+        raise RuntimeError(
+            f"_front.so cannot be loaded ({e}); build it with `python -m sparse_attention_top_ds_b200.build`") from e
+    front.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.ds_cache_quantize, lib.ds_sparse_attention_q8, lib.ds_attention_mass, lib.ds_cache_evict, lib.ds_cache_compact)))
+    _front = front
+    return front
+
 
 def _refuse(t, dtype, shape, dev, name):
     import torch
@@ -549,6 +569,16 @@ def _lead(t, dims, name):
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {list(t.shape)}")
     return t.get_device()
+
+
+def _size(t, dims, i, name):
+    """Size i of an argument of ``dims`` dimensions."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {list(t.shape)}")
+    return t.shape[i]
 
 
 def _new(like, shape, dtype, stream):
@@ -627,6 +657,10 @@ def ds_cache_quantize(rows, codes, scales, block, pos=None, length=None, stream=
     length  int32 [batch] or None (= n): how many rows are written.
     Returns (codes, scales).
     """
+    if stream is None:
+        r = (_front or _load_front()).quantize(rows, codes, scales, block, pos, length)
+        if r is not None:
+            return r
     import torch
     dev = _lead(rows, 4, "rows")
     batch, n, kv_heads, d = rows.shape
@@ -655,6 +689,10 @@ def ds_sparse_attention_q8(q, codes, scales, idx, block, scale=None, win=None, w
     Query head h reads KV head h // (heads // kv_heads).
     Returns out bf16 [batch, heads, d], or (out, lse float32 [batch, heads]).
     """
+    if stream is None and out is None and lse is None:
+        r = (_front or _load_front()).attention(q, codes, scales, idx, block, scale, win, win_len, sink, bool(return_lse))
+        if r is not None:
+            return r
     import torch
     dev = _lead(q, 3, "q")
     batch, heads, d = shape = q.shape
@@ -665,10 +703,10 @@ def ds_sparse_attention_q8(q, codes, scales, idx, block, scale=None, win=None, w
     k = W = 0
     ip = wp = None
     if idx is not None:
-        k = idx.shape[-1]
+        k = _size(idx, 2, 1, "idx")
         ip = _arg(idx, torch.int32, (batch, k), dev, "idx") if k else None
     if win is not None:
-        W = win.shape[1]
+        W = _size(win, 4, 1, "win")
         wp = _arg(win, torch.bfloat16, (batch, W, kv_heads, d), dev, "win") if W else None
     lp, sp = _opt(win_len, torch.int32, (batch,), dev, "win_len"), _opt(sink, torch.float32, (heads,), dev, "sink")
     if out is None:
@@ -699,6 +737,10 @@ def ds_attention_mass(q, cache, idx, lse, mass, scales=None, block=1, scale=None
     mass   float32 [batch, T], rows contiguous.
     Returns mass.
     """
+    if stream is None:
+        r = (_front or _load_front()).mass(q, cache, idx, lse, mass, scales, block, scale)
+        if r is not None:
+            return r
     import torch
     dev = _lead(q, 3, "q")
     batch, heads, d = shape = q.shape
@@ -713,7 +755,7 @@ def ds_attention_mass(q, cache, idx, lse, mass, scales=None, block=1, scale=None
         cstep = 0 if cache.dim() == 2 else _batch_step(cache, max(1, kv_heads * cd), "cache")
     if cd != d:
         raise ValueError("cache and q differ in d")
-    k = idx.shape[-1]
+    k = _size(idx, 2, 1, "idx")
     args = (_arg(q, torch.bfloat16, shape, dev, "q"), c, cstep, s, sstep, dt, block, T,
             _arg(idx, torch.int32, (batch, k), dev, "idx") if k else None, k,
             _arg(lse, torch.float32, (batch, heads), dev, "lse"), batch, heads, kv_heads, d,
@@ -733,6 +775,10 @@ def ds_cache_evict(mass, budget, block=1, length=None, keep_first=0, keep_last=1
     Returns (kept int32 [batch, budget]: the blocks that stay, ascending, then -1;
     new_length int32 [batch]: the rows in them).
     """
+    if stream is None and kept is None and new_length is None:
+        r = (_front or _load_front()).evict(mass, budget, block, length, keep_first, keep_last)
+        if r is not None:
+            return r
     import torch
     dev = _lead(mass, 2, "mass")
     batch, T = shape = mass.shape
@@ -768,6 +814,8 @@ def ds_cache_compact(kept, block=1, length=None, rows=(), blocks=(), stream=None
     shape, and its buffers do not overlap.  Rows of dst behind what stays are left
     as they were.
     """
+    if stream is None and (_front or _load_front()).compact(kept, block, length, rows, blocks):
+        return
     import torch
     dev = _lead(kept, 2, "kept")
     batch, budget = kept.shape

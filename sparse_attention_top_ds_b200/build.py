@@ -1,6 +1,7 @@
 """Build libdstopk.so in-tree for sm_100a with nvcc (no JIT cache), and next
 to it libdstopk_debug.so, the same library compiled with DS_DEBUG (device range
-checks that record DS_ERR_RANGE in the status word).
+checks that record DS_ERR_RANGE in the status word), and with g++ _front.so, the
+Python extension that marshals the usual calls of the 8-bit cache.
 
     python -m sparse_attention_top_ds_b200.build          # build if stale
     python -m sparse_attention_top_ds_b200.build --force  # always rebuild
@@ -17,6 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 HEADER = os.path.join(ROOT, "include", "ds_topk.h")
 LIB = os.path.join(PKG, "libdstopk.so")
 LIB_DEBUG = os.path.join(PKG, "libdstopk_debug.so")
+FRONT = os.path.join(PKG, "_front.so")
+FRONT_SOURCE = os.path.join(CSRC, "front.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -50,10 +53,39 @@ def stale(lib=LIB):
     return any(os.path.getmtime(f) > t for f in sources())
 
 
+def front_stale():
+    if not os.path.exists(FRONT):
+        return True
+    t = os.path.getmtime(FRONT)
+    return any(os.path.getmtime(f) > t for f in (HEADER, FRONT_SOURCE))
+
+
+def front_command(out):
+    """The g++ command of _front.so: the running Python's headers and its torch's."""
+    import sysconfig
+    import torch
+    gxx = shutil.which("g++")
+    if not gxx:
+        raise RuntimeError("g++ not found: cannot build _front.so")
+    home = os.path.dirname(torch.__file__)
+    include = [sysconfig.get_paths()["include"], os.path.join(home, "include"),
+               os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path()))), "include")]
+    return [gxx, "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            *(f"-I{d}" for d in include), FRONT_SOURCE, "-o", out, "-L" + os.path.join(home, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
 def build(force=False, verbose=False):
-    """Compile csrc/lib.cu into libdstopk.so and libdstopk_debug.so next to
-    this file (the two nvcc runs side by side); return the release path."""
+    """Compile csrc/lib.cu into libdstopk.so and libdstopk_debug.so and
+    csrc/front.cpp into _front.so next to this file (all side by side); return
+    the release library's path."""
     jobs = []
+    if force or front_stale():
+        cmd = front_command(FRONT + ".tmp")
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        jobs.append((FRONT, FRONT + ".tmp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
     for lib, extra in ((LIB, []), (LIB_DEBUG, ["-DDS_DEBUG"])):
         if not force and not stale(lib):
             continue
@@ -67,7 +99,7 @@ def build(force=False, verbose=False):
     for lib, tmp, proc in jobs:
         out, err = proc.communicate()
         if proc.returncode != 0:
-            errors.append(f"nvcc failed for {os.path.basename(lib)}:\n" + out + err)
+            errors.append(f"the compiler failed for {os.path.basename(lib)}:\n" + out + err)
         else:
             os.replace(tmp, lib)
     if errors:

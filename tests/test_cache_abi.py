@@ -90,6 +90,20 @@ def test_compact_arguments(lib):
         assert call(**bad) == ds.DS_ERR_ARG, bad
 
 
+def test_build_makes_the_front_extension(lib):
+    from sparse_attention_top_ds_b200 import build
+    assert not build.front_stale()
+    front = _native._load_front()
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    for call in (lambda: front.quantize(q, q, q, 1, None, None), lambda: front.attention(q, q, q, q, 1, None, None, None, None, True),
+                 lambda: front.mass(q, q, q, q, q, None, 1, None), lambda: front.evict(q, 1, 1, None, 0, 1),
+                 lambda: front.compact(q, 1, None, [], []), lambda: front.quantize(), lambda: front.attention(None, 1, "x"),
+                 lambda: front.evict(3, "x", None, q, -1, 2 ** 70)):
+        assert call() is None            # nothing that is not the usual call is taken
+    with pytest.raises(TypeError):
+        front.bind(1, 2)
+
+
 def test_front_end_refuses_tensors_off_the_gpu():
     x = torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16)
     codes, scales = torch.zeros(2, 8, 1, 64, dtype=torch.int8), torch.zeros(2, 8, 1)

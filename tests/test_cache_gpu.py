@@ -47,9 +47,11 @@ def dec(bits):
     return inputs.bf16_bits_to_f32(bits).astype(np.float64)
 
 
-def ok_status():
+def ok_status(skipped=False):
+    """No error on the device; ``skipped``: slots outside [0, T) or rows past a cache's end were given, which the
+    debug build records."""
     torch.cuda.synchronize()
-    assert ds.ds_get_device_status() == ds.DS_OK
+    assert ds.ds_get_device_status() in ((ds.DS_OK, ds.DS_ERR_RANGE) if skipped and ds.ds_debug_build() else (ds.DS_OK,))
 
 
 def quantized(rows, block, fmt):
@@ -94,7 +96,7 @@ def test_quantize_matches_the_oracle(cuda_device, case):
     ln = None if length is None else i32_to_device(np.array(length))
     r = ds.ds_cache_quantize(bf16_to_device(rows), gc, gs, block, pos=p, length=ln)
     assert r[0] is gc and r[1] is gs
-    ok_status()
+    ok_status(skipped=T < n + max(pos or [0]))  # rows past the cache's end are cut
     for b in range(B):
         m = n if length is None else length[b]
         at = 0 if pos is None else pos[b]
@@ -254,7 +256,7 @@ def check_attention(case, a, out, lse, scale=None):
 def test_attention_matches_the_oracle(cuda_device, case):
     a = attend_inputs(case)
     (out, lse), _ = attend(case, a)
-    ok_status()
+    ok_status(skipped=case[11] > 0)
     check_attention(case, a, out, lse)
 
 
@@ -410,6 +412,8 @@ MASS = [
     (2, 9, 1, 448, 60, 60, 1, "bf16", False, 0.5),
     (2, 33, 3, 64, 40, 33, 1, "e4m3", True, 0.0),
     (4, 128, 1, 128, 700, 640, 1, "bf16", True, 0.0),
+    (2, 48, 12, 64, 50, 20, 4, "int8", False, 0.1),     # more KV heads than a cluster has CTAs
+    (1, 640, 1, 192, 90, 70, 8, "e4m3", False, 0.0),    # more head tiles than that
 ]
 
 
@@ -457,12 +461,12 @@ def check_mass(case, a, mass, times=1):
 def test_mass_matches_the_oracle(cuda_device, case):
     a = mass_inputs(case)
     mass = account(case, a)
-    torch.cuda.synchronize()
-    assert ds.ds_get_device_status() in ((ds.DS_OK, ds.DS_ERR_RANGE) if case[9] and ds.ds_debug_build() else (ds.DS_OK,))
+    ok_status(skipped=case[9] > 0)
     check_mass(case, a, mass)
     check_mass(case, a, account(case, a, mass=mass), times=2)
     again = account(case, a)
     assert np.array_equal(bits_of(again), bits_of(account(case, a)))
+    ok_status(skipped=case[9] > 0)
 
 
 def test_mass_heads_without_a_softmax_add_nothing(cuda_device):
@@ -519,6 +523,19 @@ def evict(mass, case, length=None, **kw):
                           keep_last=last, **kw)
     ok_status()
     return r[0].cpu().numpy(), r[1].cpu().numpy()
+
+
+@pytest.mark.parametrize("T,block,budget", [(500_000, 1, 300_000), (3_000_000, 2, 1_000_000), (3_000_000, 128, 20_000)])
+def test_evict_long_rows(cuda_device, T, block, budget):
+    # more blocks to a CTA than it holds keys of; whole-number accounts, so that there are ties and sums are exact
+    m = torch.randint(0, 1000, (2, T), device="cuda", generator=torch.Generator("cuda").manual_seed(5)).float()
+    kept, n = ds.ds_cache_evict(m, budget, block=block, keep_first=3, keep_last=5)
+    ok_status()
+    nb = -(-T // block)
+    key = torch.nn.functional.pad(m, (0, nb * block - T)).view(2, nb, block).sum(-1)
+    key[:, :3], key[:, nb - 5:] = 1e9, 1e9
+    want = key.sort(dim=1, descending=True, stable=True).indices[:, :budget].sort(dim=1).values
+    assert torch.equal(kept.long(), want) and n.tolist() == [budget * block - (nb * block - T)] * 2
 
 
 @pytest.mark.parametrize("kind", ["tail", "ties", "zeros", "special"])
@@ -592,6 +609,31 @@ def test_compact_moves_every_array(cuda_device, case):
     for s, d, (raw, c, per_block) in zip(src, dst, arrays):
         want = oracle.compact(raw, np.full((B, c) + raw.shape[2:], 77, raw.dtype), kept, ln, block, per_block)
         assert np.array_equal(d.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("block,width,budget", [(16, 256, 3000), (64, 1040, 500), (4, 4096, 2000), (1, 16, 9000)])
+def test_compact_many_blocks(cuda_device, block, width, budget):
+    # many more pieces than a CTA has stages, two large arrays and two small ones, a short last block
+    T, B = 60_001 if block > 1 else 10_001, 2
+    g = torch.Generator("cuda").manual_seed(block)
+    nb = -(-T // block)
+    src = [torch.randint(0, 256, (B, T, width), device="cuda", dtype=torch.uint8, generator=g),
+           torch.randint(0, 2 ** 31 - 1, (B, T), device="cuda", dtype=torch.int32, generator=g),
+           torch.randint(0, 256, (B, T, width // 2), device="cuda", dtype=torch.uint8, generator=g)]
+    scales = torch.rand(B, nb, 3, device="cuda", generator=g)
+    kept = torch.stack([torch.randperm(nb, device="cuda", generator=g)[:budget].sort().values for _ in range(B)]).int()
+    kept[1, -1] = nb - 1
+    m = min(T, budget * block)
+    dst = [torch.zeros((B, m) + s.shape[2:], dtype=s.dtype, device="cuda") for s in src]
+    to = torch.zeros(B, budget, 3, device="cuda")
+    ds.ds_cache_compact(kept, block=block, rows=list(zip(src, dst)), blocks=[(scales, to)])
+    ok_status()
+    at = (kept.long()[:, :, None] * block + torch.arange(block, device="cuda")).view(B, -1)[:, :m]
+    b = torch.arange(B, device="cuda")[:, None]
+    for s, d in zip(src, dst):
+        there = (at < T).view((B, m) + (1,) * (s.dim() - 2))
+        assert torch.equal(d, torch.where(there, s[b, at.clamp_max(T - 1)], torch.zeros_like(d)))
+    assert torch.equal(to, scales[b, kept.long()])
 
 
 def test_compact_any_list_stays_inside(cuda_device):
@@ -762,6 +804,35 @@ def test_a_stream_argument_other_than_the_current_one(cuda_device):
     assert torch.equal(out, o2) and torch.equal(lse, l2) and kept.shape == (2, 7)
 
 
+def test_both_ways_of_marshalling_agree(cuda_device, monkeypatch):
+    # the extension takes these calls, and the binding's own marshalling gives the same bits
+    from sparse_attention_top_ds_b200 import _native
+    a = serve_inputs(26)
+    taken = {}
+
+    class Spy:
+        def __getattr__(self, name):
+            def call(*args):
+                r = getattr(front, name)(*args)
+                taken.setdefault(name, []).append(r is not None)
+                return r
+            return call
+
+    front = _native._front or _native._load_front()
+    monkeypatch.setattr(_native, "_front", Spy())
+    by_front = serve(*a)
+    assert {k: all(v) for k, v in taken.items()} == dict.fromkeys(("quantize", "attention", "mass", "evict", "compact"), True)
+
+    class Off:
+        def __getattr__(self, name):
+            return lambda *args: None
+
+    monkeypatch.setattr(_native, "_front", Off())
+    for x, y in zip(by_front, serve(*a)):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    test_front_end_refusals(cuda_device)
+
+
 def test_captured_runs_replay_on_new_inputs_side_by_side(cuda_device):
     # two graphs of the whole run, replayed at once on two streams with inputs changed in place
     a, b = serve_inputs(24), serve_inputs(25)
@@ -792,14 +863,18 @@ def test_captured_runs_replay_on_new_inputs_side_by_side(cuda_device):
         assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(r, w))
 
 
-@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
-def test_results_on_many_batch_rows_do_not_depend_on_the_batch(cuda_device, fmt):
-    # a batch row alone and among 200 others, over a shared cache: within the bounds of both (work is split differently)
-    case = (200, 64, 1, 256, 400, 150, 0, 16, fmt, True, False, 0.0, None)
+@pytest.mark.parametrize("case", [(200, 64, 1, 256, 400, 150, 0, 16, "e4m3", True, False, 0.0, None),
+                                  (200, 64, 1, 256, 400, 150, 0, 16, "int8", True, False, 0.0, None),
+                                  (160, 20, 1, 448, 600, 300, 130, 4, "int8", True, True, 0.1, None),
+                                  (300, 40, 2, 64, 700, 513, 3, 1, "e4m3", True, False, 0.3, None),
+                                  (150, 128, 1, 512, 900, 400, 65, 64, "e4m3", True, True, 0.0, None),
+                                  (33, 33, 1, 384, 300, 257, 0, 8, "int8", True, True, 0.0, None)],
+                         ids=lambda c: "x".join(map(str, c[:10])))
+def test_attention_on_many_batch_rows(cuda_device, case):
+    # as many batch rows as fill the GPU, so that a CTA passes through all chunks of its rows: the first and last of them
     a = attend_inputs(case)
     (out, lse), t = attend(case, a)
-    ok_status()
-    few = dict(a, q=a["q"][:3], idx=a["idx"][:3])
-    check_attention((3,) + case[1:], few, out[:3], lse[:3])
-    few = dict(a, q=a["q"][197:], idx=a["idx"][197:])
-    check_attention((3,) + case[1:], few, out[197:], lse[197:])
+    ok_status(skipped=case[11] > 0)
+    for s in (slice(0, 2), slice(case[0] - 2, case[0])):
+        few = dict(a, q=a["q"][s], idx=a["idx"][s], win=None if a["win"] is None else a["win"][s])
+        check_attention((2,) + case[1:], few, out[s], lse[s])
