@@ -67,30 +67,21 @@ __device__ __forceinline__ uint32_t ce_key(const CeParams& p, const float* mass,
   return ce_order(sum);
 }
 
-// Sum over the CTA's threads before this one, and over all of them.
-__device__ __forceinline__ uint64_t ce_scan(uint64_t v, uint64_t* warp_s, uint64_t* total) {
+// Sum over the CTA's threads before this one, and over all of them.  One barrier:
+// the next scan takes another `warp_s`.
+__device__ __forceinline__ uint32_t ce_scan(uint32_t v, uint32_t* warp_s, uint32_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint64_t x = v;
+  uint32_t x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  __syncthreads();
   if (lane == 31) warp_s[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    uint64_t w = warp_s[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    warp_s[lane] = w;
-  }
-  __syncthreads();
-  *total = warp_s[31];
-  return (warp > 0 ? warp_s[warp - 1] : 0) + x - v;
+  const uint32_t t = warp_s[lane];
+  *total = __reduce_add_sync(0xffffffffu, t);
+  return __reduce_add_sync(0xffffffffu, lane < warp ? t : 0u) + x - v;
 }
 
 __device__ __forceinline__ uint2 dsmem_ld_u32x2(uint32_t addr) {
@@ -99,12 +90,39 @@ __device__ __forceinline__ uint2 dsmem_ld_u32x2(uint32_t addr) {
   return v;
 }
 
+// The keys of blocks n0 .. n0 + held - 1: a warp reads 32 rows at a time, min(block,
+// 32) lanes to a block and STEPS reads to each, with 8 reads in flight.
+template <int STEPS>
+__device__ __forceinline__ void ce_keys(const CeParams& p, const float* mass, uint32_t* keys, int n0, int held, int nb, int L) {
+  constexpr int kSets = 8 / STEPS;  // of 32 / span blocks
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int span = min(p.block, 32), per = 32 / span, sub = lane / span;
+  for (int i0 = warp * per * kSets; i0 < held; i0 += kCeThreads / 32 * per * kSets) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + (u / STEPS) * per + sub, r = (n0 + i) * p.block + lane % span + (u % STEPS) * 32;
+      v[u] = i < held && r < L ? __ldcg(mass + r) : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < kSets; ++u) {
+      double sum = (double)v[u * STEPS];
+#pragma unroll
+      for (int e = 1; e < STEPS; ++e) sum += (double)v[u * STEPS + e];
+      for (int o = span >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const int i = i0 + u * per + sub;
+      if (i < held && lane % span == 0) keys[i] = ce_protected(p, n0 + i, nb) ? 0xffffffffu : ce_order(sum);
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kCeThreads) cache_evict_kernel(const CeParams p) {
   extern __shared__ uint32_t keys[];                // [min(share, kCeKeys)]
   __shared__ uint32_t hist[2][kCeBins];             // a digit's counts; two, so that one barrier parts two digits
-  __shared__ uint64_t warp_s[32];
+  __shared__ uint32_t warp_s[2][32];
   __shared__ uint32_t found[3];                     // digit of the last key, blocks to take of it, blocks that have it
-  __shared__ uint64_t counts;                       // this CTA's (blocks above the key) << 32 | (equal to it)
+  __shared__ uint2 counts;                          // this CTA's blocks above the key, and equal to it
+  __shared__ uint32_t earlier[2];                   // the same over the CTAs before
   const int tid = threadIdx.x, lane = tid & 31;
   const int C = (int)cluster_nctarank(), rank = (int)cluster_ctarank(), b = blockIdx.x / C;
   if (C > 1) cluster_arrive_relaxed();
@@ -122,28 +140,14 @@ __global__ void __launch_bounds__(kCeThreads) cache_evict_kernel(const CeParams 
   auto key = [&](int n) { return n - n0 < held ? keys[n - n0] : ce_key(p, mass, n, nb, L); };
   uint32_t prefix = 0;
   int need = p.budget;
-  uint64_t above = 0;  // blocks that stay in the CTAs before this one: above << 32 | equal
 
   if (!all) {
-    // the keys held: a warp reads 32 rows at a time, `span` lanes to a block, four of
-    // these at once
-    const int span = min(p.block, 32), per = 32 / span, sub = lane / span;
-    for (int i0 = (tid >> 5) * per * 4; i0 < held; i0 += kCeThreads / 32 * per * 4) {
-      double sum[4] = {0.0, 0.0, 0.0, 0.0};
-      for (int o = lane % span; o < p.block; o += span) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int i = i0 + u * per + sub, r = (n0 + i) * p.block + o;
-          if (i < held && r < L) sum[u] += (double)__ldcg(mass + r);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int i = i0 + u * per + sub;
-        for (int o = span >> 1; o > 0; o >>= 1) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
-        if (i < held && lane % span == 0) keys[i] = ce_protected(p, n0 + i, nb) ? 0xffffffffu : ce_order(sum[u]);
-      }
-    }
+    if (p.block == 128)
+      ce_keys<4>(p, mass, keys, n0, held, nb, L);
+    else if (p.block == 64)
+      ce_keys<2>(p, mass, keys, n0, held, nb, L);
+    else
+      ce_keys<1>(p, mass, keys, n0, held, nb, L);
     __syncthreads();
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kCeBins;
@@ -172,8 +176,8 @@ __global__ void __launch_bounds__(kCeThreads) cache_evict_kernel(const CeParams 
       }
       if (pass < 2)
         for (int i = tid; i < kCeBins; i += kCeThreads) hist[(pass + 1) & 1][i] = 0;
-      uint64_t total;
-      const uint32_t before = (uint32_t)ce_scan(c1 + c0, warp_s, &total);
+      uint32_t total;
+      const uint32_t before = ce_scan(c1 + c0, warp_s[pass & 1], &total);
       if (hi > 0 && before < (uint32_t)need && before + c1 + c0 >= (uint32_t)need) {
         const bool first = before + c1 >= (uint32_t)need;
         found[0] = (uint32_t)(first ? hi : hi - 1);
@@ -205,26 +209,22 @@ __global__ void __launch_bounds__(kCeThreads) cache_evict_kernel(const CeParams 
     }
   else
     gt = (uint32_t)(t1 - t0);
-  uint64_t total;
-  uint64_t mine = ce_scan((uint64_t)gt << 32 | eq, warp_s, &total);
+  uint32_t all_gt, all_eq = 0;
+  __syncthreads();
+  uint32_t ngt = ce_scan(gt, warp_s[0], &all_gt), neq = 0;
+  if (need > 0) neq = ce_scan(eq, warp_s[1], &all_eq);  // (without ties to part, equal blocks do not count)
   if (C > 1) {
-    if (tid == 0) counts = total;
+    if (tid == 0) counts = make_uint2(all_gt, all_eq);
     cluster_sync();
     if (tid < 32) {
-      uint64_t v = 0;
-      if (lane < rank) {
-        const uint2 x = dsmem_ld_u32x2(dsmem_map(smem_u32(&counts), (uint32_t)lane));
-        v = (uint64_t)x.y << 32 | x.x;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == 0) warp_s[0] = v;
+      const uint2 c = lane < rank ? dsmem_ld_u32x2(dsmem_map(smem_u32(&counts), (uint32_t)lane)) : make_uint2(0u, 0u);
+      const uint32_t x = __reduce_add_sync(0xffffffffu, c.x), y = __reduce_add_sync(0xffffffffu, c.y);
+      if (lane == 0) earlier[0] = x, earlier[1] = y;
     }
     __syncthreads();
-    above = warp_s[0];
+    ngt += earlier[0];
+    neq += earlier[1];
   }
-  mine += above;
-  uint32_t ngt = (uint32_t)(mine >> 32), neq = (uint32_t)mine;
   for (int n = t0; n < t1; ++n) {
     const uint32_t k = all ? 1u : key(n);
     const bool is_eq = !all && k == prefix, stays = all || k > prefix || (is_eq && neq < (uint32_t)need);
