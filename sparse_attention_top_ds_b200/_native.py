@@ -495,6 +495,7 @@ _front = None
 def _load_front():
     """Import the extension once and give it the library's addresses."""
     global _front
+    import torch  # noqa: F401  (loads the libraries that the extension is linked to)
     lib = load()
     try:
         from . import _front as front

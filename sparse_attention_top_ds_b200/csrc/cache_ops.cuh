@@ -233,13 +233,13 @@ extern "C" int ds_sparse_attention_q8(const void* q, const void* codes, int64_t 
   p.log_block = cache_log_block(block);
   p.scale_log2 = scale * 1.4426950408889634f;
   // Heads of a CTA, CTAs of a tile (while all tiles' clusters run at once) and rows
-  // of a chunk.  Measured at 512 channels, a CTA's turn of a chunk takes 3.6, 4.0 and
-  // 4.7 us with 16, 32 and 64 heads (the MMAs cost the same up to 64), the parts of a
-  // call beside its turns 5, 5 and 9 us, and 7.7, 8.7 and 13.6 where a cluster
+  // of a chunk.  Measured at 512 channels, a CTA's turn of a chunk takes 3.2, 3.5 and
+  // 4.4 us with 16, 32 and 64 heads (the MMAs cost the same up to 64), the parts of a
+  // call beside its turns 5.5, 5.5 and 8.5 us, and 7.1, 8.1 and 12.9 where a cluster
   // exchanges partial results; what has the least of both, over all waves of CTAs, is
-  // taken.  128 heads over 1024 + 128 rows: one batch row 16 heads, 9 CTAs 11.4 us
-  // (64, 9: 18.3), eight 32, 4 20.4 us (64, 6: 23.0), thirty-two 64, 2 37.2 us (32, 1:
-  // 40.4).
+  // taken.  128 heads over 1024 + 128 rows: one batch row 16 heads, 9 CTAs 10.3 us
+  // (64, 10: 17), eight 32, 4 18.4 us (64, 6: 21.5), thirty-two 64, 2 35.0 us (32, 1:
+  // 37.3).
   const int G = heads / kv_heads;
   auto turns = [&](int r, int c) { return ((k + r - 1) / r + (W + r - 1) / r + c - 1) / c; };
   int n = 0;
@@ -248,7 +248,7 @@ extern "C" int ds_sparse_attention_q8(const void* q, const void* codes, int64_t 
   static const struct {
     int n;
     double turn, alone, cluster;
-  } kCost[] = {{16, 3.6, 5.0, 7.7}, {32, 4.0, 5.0, 8.7}, {64, 4.7, 9.0, 13.6}};
+  } kCost[] = {{16, 3.2, 5.5, 7.1}, {32, 3.5, 5.5, 8.1}, {64, 4.4, 8.5, 12.9}};
   for (const auto& w : kCost) {
     const int64_t t = (int64_t)batch * kv_heads * ((G + w.n - 1) / w.n);
     for (int c = 1; c <= kAqMaxCluster; ++c) {
@@ -355,9 +355,9 @@ extern "C" int ds_cache_evict(const float* mass, int64_t mass_batch_stride, int 
   p.budget = budget;
   p.first = keep_first;
   p.last = keep_last;
-  // CTAs of a batch row: a share of more than 8192 rows to each (8 rows of 32768 in
-  // blocks of 64 took 12.1 us with 2 CTAs each, 14.7 with 8: reading the others' counts
-  // costs more than it saves)
+  // CTAs of a batch row: a share of some 8192 rows to each.  8 rows of 32768 in blocks
+  // of 64 took 10.3 us with 4 CTAs each, 11.1 with 2 and 13.1 with 8 (every CTA reads
+  // the others' counts); in blocks of 1 16.7, 27.7 and 16.3.
   int C = 1;
   while (C < kCeMaxCluster && T / C > 8192) C *= 2;
   const int nb = (T + block - 1) / block;
