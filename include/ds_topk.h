@@ -403,9 +403,9 @@ int ds_cache_quantize(const void* rows, int64_t rows_batch_stride, int64_t row_s
  * win      device bfloat16 [batch, W, kv_heads, d] or NULL (then W must be 0);
  *          16-byte aligned; 0 <= W <= DS_ATTN_MAX_WINDOW.
  * kv_heads divides heads.
- * Scales and window rows are expected to be finite; what is attended and not
- * finite makes the outputs of its KV head's query heads NaN.  Rows and scales
- * that no slot names are not read.
+ * Scales and window rows are expected to be finite; a NaN that is attended (a
+ * code, a scale or a window value) makes the outputs of its KV head's query heads
+ * NaN.  Rows and scales that no slot names do not matter.
  * Returns DS_OK, DS_ERR_ARG, DS_ERR_UNSUPPORTED or DS_ERR_CUDA.
  */
 int ds_sparse_attention_q8(const void* q, const void* codes, int64_t codes_batch_stride, const float* scales,
@@ -493,7 +493,7 @@ typedef struct {
  *          int32 [batch] or NULL (= T); T 1 .. 16777216 rows of every src.
  * Batch strides, if batch > 1, are at least the bytes of a batch row: src T
  * items (ceil(T / block) with per_block), dst min(T, budget * block) (budget).
- * src and dst of an array must not overlap (DS_ERR_ARG).
+ * No array's dst may overlap an array's src (DS_ERR_ARG).
  * Returns DS_OK, DS_ERR_ARG, DS_ERR_UNSUPPORTED or DS_ERR_CUDA.
  */
 int ds_cache_compact(const ds_cache_array* arrays, int n_arrays, const int32_t* kept, int budget, const int32_t* len,

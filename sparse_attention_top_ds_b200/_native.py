@@ -812,7 +812,7 @@ def ds_cache_compact(kept, block=1, length=None, rows=(), blocks=(), stream=None
     blocks  pairs with one entry for each block, [batch, ceil(T / block), ...] and
             [batch, at least budget, ...] (scales).
     The arrays are contiguous behind the batch; a pair has one dtype and trailing
-    shape, and its buffers do not overlap.  Rows of dst behind what stays are left
+    shape, and no dst overlaps a src.  Rows of dst behind what stays are left
     as they were.
     """
     if stream is None and (_front or _load_front()).compact(kept, block, length, rows, blocks):

@@ -136,10 +136,14 @@ __device__ __forceinline__ void aq_store(const uint4 (&v)[4 * K], int m, int n, 
         lo = swap_middle(v[k * 4 + e * 2]), hi = swap_middle(v[k * 4 + e * 2 + 1]);
       } else {
         const uint4 x = v[k * 4 + (m & 1) * 2 + e];
-        decode8x4<FMT>(x.x, lo.x, lo.y);
-        decode8x4<FMT>(x.y, lo.z, lo.w);
-        decode8x4<FMT>(x.z, hi.x, hi.y);
-        decode8x4<FMT>(x.w, hi.z, hi.w);
+        uint32_t top = 0;
+        decode8x4<FMT>(x.x, lo.x, lo.y, top);
+        decode8x4<FMT>(x.y, lo.z, lo.w, top);
+        decode8x4<FMT>(x.z, hi.x, hi.y, top);
+        decode8x4<FMT>(x.w, hi.z, hi.w, top);
+        // one NaN makes the row's scores NaN, wherever it is.  (The check takes 560 us to
+        // 587 at 512 tokens over 2048 rows, and 19.1 to 19.5 in the decode call.)
+        if (FMT == kFmtE4m3 && e4m3_nan(top)) lo.x = 0x7fc07fc0u;
       }
       const uint32_t at = at0 + (uint32_t)(e * kAqBlock + k * 64 * 128);
       sts128(at, lo);

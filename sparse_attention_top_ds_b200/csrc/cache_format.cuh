@@ -53,15 +53,17 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax) {
 // channels 1 and 2 of every 4 exchanged (swap_middle does it to other operands).
 //  * e4m3: the 4 exponent and 3 mantissa bits are moved into a bfloat16's
 //    fields, which gives the value times 2^-120 (the exponent biases are 7 and
-//    127; subnormal codes become subnormal values), and multiplied by 2^120.
+//    127; subnormal codes become subnormal values), and multiplied by 2^120.  That
+//    reads NaN as 480: `top` collects the largest such fields for e4m3_nan.
 //  * int8: with s the sign bit and l the low 7 bits the value is
 //    (128 + l) - (128 + 128 s), and both terms are 0x4300 with bits or-ed in.
 template <int FMT>
-__device__ __forceinline__ void decode8x4(uint32_t w, uint32_t& even, uint32_t& odd) {
+__device__ __forceinline__ void decode8x4(uint32_t w, uint32_t& even, uint32_t& odd, uint32_t& top) {
   if constexpr (FMT == kFmtE4m3) {
     const uint32_t k = 0x7b807b80u;  // 2^120 twice
-    even = ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u);
-    odd = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
+    even = (w << 4) & 0x07f007f0u, odd = (w >> 4) & 0x07f007f0u;
+    top = __vmaxu2(__vmaxu2(top, even), odd);  // (cheaper than a look at the codes' bytes)
+    even |= (w << 8) & 0x80008000u, odd |= w & 0x80008000u;
     asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(even) : "r"(k));
     asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(odd) : "r"(k));
   } else {
@@ -70,6 +72,9 @@ __device__ __forceinline__ void decode8x4(uint32_t w, uint32_t& even, uint32_t& 
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(odd) : "r"((v & 0x007f007fu) | k), "r"((v & 0x00800080u) | k));
   }
 }
+
+// Was there a NaN among the codes of these largest fields?
+__device__ __forceinline__ bool e4m3_nan(uint32_t top) { return ((top + 0x00100010u) & 0x08000800u) != 0; }
 
 // 8 values of 16 bits with the middle two of every 4 exchanged.
 __device__ __forceinline__ uint4 swap_middle(const uint4& x) {

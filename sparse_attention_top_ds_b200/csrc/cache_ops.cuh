@@ -51,8 +51,18 @@ static AqKernel aq_kernel(int dtype, int n) {
     return n == 16 ? attn_q8_kernel<kFmtE4m3, 16> : n == 32 ? attn_q8_kernel<kFmtE4m3, 32> : attn_q8_kernel<kFmtE4m3, 64>;
   return n == 16 ? attn_q8_kernel<kFmtI8, 16> : n == 32 ? attn_q8_kernel<kFmtI8, 32> : attn_q8_kernel<kFmtI8, 64>;
 }
+// Shared memory that a CTA of the attention or the account asks for at least.  Its
+// cluster waits for all its CTAs, and a CTA waits for its tensor memory: two clusters
+// that met on two SMs, each with the tensor memory that the other waits for, would
+// wait for good.  With this much, no two CTAs of kernels that have both (these two,
+// and the two below) fit one SM.  (Registers part them too, as compiled today.)
+constexpr int kCacheAlone = 176 * 1024;
+constexpr int kSmSmem = 228 * 1024, kCtaSmem = 1024;  // of an SM, and what a CTA takes besides its own
+static_assert(2 * (kCacheAlone + kCtaSmem) > kSmSmem, "two CTAs of the 8-bit cache on an SM");
+static_assert(kCacheAlone + PvSmem<1, 2>::bytes(1) + 2 * kCtaSmem > kSmSmem, "one beside the 16-bit attention's");
+static_assert(kCacheAlone + QtSmem::kBytes + 2 * kCtaSmem > kSmSmem, "one beside the query projection's");
 static int aq_smem(int n, int D) {
-  return n == 16 ? AqSmem<16>::bytes(D) : n == 32 ? AqSmem<32>::bytes(D) : AqSmem<64>::bytes(D);
+  return std::max(kCacheAlone, n == 16 ? AqSmem<16>::bytes(D) : n == 32 ? AqSmem<32>::bytes(D) : AqSmem<64>::bytes(D));
 }
 
 // The account's.
@@ -64,7 +74,7 @@ static AqKernel am_kernel(int dtype, int n) {
   return n == 16 ? attn_mass_kernel<kFmtI8, 16> : n == 32 ? attn_mass_kernel<kFmtI8, 32> : attn_mass_kernel<kFmtI8, 64>;
 }
 static int am_smem(int n, int D) {
-  return n == 16 ? AmSmem<16>::bytes(D) : n == 32 ? AmSmem<32>::bytes(D) : AmSmem<64>::bytes(D);
+  return std::max(kCacheAlone, n == 16 ? AmSmem<16>::bytes(D) : n == 32 ? AmSmem<32>::bytes(D) : AmSmem<64>::bytes(D));
 }
 
 static void cache_cluster(cudaLaunchAttribute& a, int C) {
@@ -384,6 +394,7 @@ extern "C" int ds_cache_compact(const ds_cache_array* arrays, int n_arrays, cons
   if (budget < 1 || budget > nb || cache_misaligned(kept, 4) || cache_misaligned(len, 4)) return DS_ERR_ARG;
   if ((int64_t)batch * budget > INT32_MAX) return DS_ERR_ARG;
   CcParams p = {};
+  std::pair<uintptr_t, uintptr_t> src[DS_CACHE_MAX_ARRAYS], dst[DS_CACHE_MAX_ARRAYS];
   for (int i = 0; i < n_arrays; ++i) {
     const ds_cache_array& a = arrays[i];
     if (!a.src || !a.dst || a.item_bytes < 1 || a.item_bytes > (int64_t(1) << 24) || (a.per_block != 0 && a.per_block != 1))
@@ -391,11 +402,9 @@ extern "C" int ds_cache_compact(const ds_cache_array* arrays, int n_arrays, cons
     const int64_t src_bytes = a.item_bytes * (a.per_block ? nb : T);
     const int64_t dst_bytes = a.item_bytes * (a.per_block ? budget : std::min<int64_t>(T, (int64_t)budget * block));
     if (batch > 1 && (a.src_batch_stride < src_bytes || a.dst_batch_stride < dst_bytes)) return DS_ERR_ARG;
-    // the moves are not ordered among themselves, so the buffers may not overlap
     const uintptr_t s0 = reinterpret_cast<uintptr_t>(a.src), d0 = reinterpret_cast<uintptr_t>(a.dst);
-    const uintptr_t s1 = s0 + (uintptr_t)((batch - 1) * a.src_batch_stride + src_bytes);
-    const uintptr_t d1 = d0 + (uintptr_t)((batch - 1) * a.dst_batch_stride + dst_bytes);
-    if (s0 < d1 && d0 < s1) return DS_ERR_ARG;
+    src[i] = {s0, s0 + (uintptr_t)((batch - 1) * a.src_batch_stride + src_bytes)};
+    dst[i] = {d0, d0 + (uintptr_t)((batch - 1) * a.dst_batch_stride + dst_bytes)};
     const uint64_t bits = (uint64_t)s0 | d0 | (uint64_t)a.item_bytes |
                           (batch > 1 ? (uint64_t)a.src_batch_stride | (uint64_t)a.dst_batch_stride : 0);
     CcArray& c = p.a[i];
@@ -407,6 +416,10 @@ extern "C" int ds_cache_compact(const ds_cache_array* arrays, int n_arrays, cons
     c.per_block = a.per_block;
     c.vec = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
   }
+  // the moves are not ordered among themselves, so no array may be written where one is read
+  for (int i = 0; i < n_arrays; ++i)
+    for (int j = 0; j < n_arrays; ++j)
+      if (src[i].first < dst[j].second && dst[j].first < src[i].second) return DS_ERR_ARG;
   DeviceState* s = nullptr;
   const int rc = device_state(&s);
   if (rc != DS_OK) return rc;
@@ -420,7 +433,7 @@ extern "C" int ds_cache_compact(const ds_cache_array* arrays, int n_arrays, cons
   p.B = batch;
   p.wait_ns = wait_limit();
   // Arrays with blocks of 4 KiB and more, in multiples of 16 bytes, go by bulk
-  // copies, ahead of the others: 67 MB of 32 KiB blocks moved in 22 us, against 30 us
+  // copies, ahead of the others: 67 MB of 32 KiB blocks moved in 24 us, against 30 us
   // by the threads; below that a copy's fixed cost is as large as its bytes'.
   std::stable_partition(p.a, p.a + p.n, [&](CcArray& c) {
     const int64_t unit = c.item * (c.per_block ? 1 : block);

@@ -90,6 +90,17 @@ def test_compact_arguments(lib):
         assert call(**bad) == ds.DS_ERR_ARG, bad
 
 
+def test_compact_refuses_an_array_written_where_another_is_read(lib):
+    def call(*arrays):
+        arr = b"".join(struct.pack(_native._CACHE_ARRAY, src, dst, 102400, 65536, 1024, 0) for src, dst in arrays)
+        return lib.ds_cache_compact(arr, len(arrays), A, 4, None, 2, 100, 16, None)
+
+    first = (0x100000, 0x900000)
+    for second in ((0x900000, 0x1100000), (0x900000 + 65536 + 65535, 0x1100000), (0x1100000, 0x100000),
+                   (0x1100000, 0x100000 + 204799)):
+        assert call(first, second) == call(second, first) == ds.DS_ERR_ARG, second
+
+
 def test_build_makes_the_front_extension(lib):
     from sparse_attention_top_ds_b200 import build
     assert not build.front_stale()

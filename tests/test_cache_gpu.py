@@ -343,6 +343,22 @@ def test_attention_over_a_block_that_is_not_finite_is_nan(cuda_device):
     assert np.isnan(lse.cpu().numpy()[1, 4:]).all() and np.isfinite(lse.cpu().numpy()[0]).all()
 
 
+@pytest.mark.parametrize("heads", [(8, 2), (20, 1), (130, 2)], ids=str)
+@pytest.mark.parametrize("code,channel", [(0x7F, 0), (0xFF, 129), (0x7F, 191), (0xFF, 62)])
+def test_attention_over_a_nan_code_is_nan(cuda_device, heads, code, channel):
+    H, K = heads
+    case = (2, H, K, 192, 700, 600, 30, 4, "e4m3", False, False, 0.0, None)
+    a = attend_inputs(case)
+    (out, lse), _ = attend(case, a)
+    a["codes"][1, a["idx"][1, 301], K - 1, channel] = code
+    (out2, lse2), _ = attend(case, a)
+    ok_status()
+    hit = np.zeros((2, H), bool)
+    hit[1, H - H // K:] = True  # the heads of the last KV head of batch row 1
+    assert np.isnan(dec(bits_of(out2))[hit]).all() and np.isnan(lse2.cpu().numpy()[hit]).all()
+    assert np.array_equal(bits_of(out)[~hit], bits_of(out2)[~hit]) and np.array_equal(bits_of(lse)[~hit], bits_of(lse2)[~hit])
+
+
 def test_attention_every_code(cuda_device):
     # one-hot queries on a single row read the row itself: all finite codes of both formats come back exactly
     for fmt in ("e4m3", "int8"):
@@ -476,6 +492,19 @@ def test_mass_heads_without_a_softmax_add_nothing(cuda_device):
     a["lse"][1, 3:66] = -np.inf
     check_mass(case, a, account(case, a))
     ok_status()
+
+
+@pytest.mark.parametrize("code,channel", [(0x7F, 0), (0xFF, 129), (0x7F, 191), (0xFF, 62)])
+def test_mass_of_a_row_with_a_nan_code_is_nan(cuda_device, code, channel):
+    case = (2, 24, 2, 192, 300, 200, 4, "e4m3", False, 0.0)
+    a = mass_inputs(case)
+    mass, row = account(case, a), a["idx"][1, 77]
+    a["codes"][1, row, 1, channel] = code
+    got = account(case, a)
+    ok_status()
+    assert torch.isnan(got[1, row])
+    got[1, row] = mass[1, row]
+    assert np.array_equal(bits_of(mass), bits_of(got))
 
 
 def test_mass_strided_accounts_repeated_slots_and_no_slots(cuda_device):
