@@ -415,6 +415,8 @@ extern "C" int ds_cache_compact(const ds_cache_array* arrays, int n_arrays, cons
     c.item = a.item_bytes;
     c.per_block = a.per_block;
     c.vec = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
+    c.row_per = (uint32_t)(c.item / c.vec);
+    c.per = (uint32_t)(a.per_block ? 1 : block) * c.row_per;
   }
   // the moves are not ordered among themselves, so no array may be written where one is read
   for (int i = 0; i < n_arrays; ++i)
@@ -432,23 +434,29 @@ extern "C" int ds_cache_compact(const ds_cache_array* arrays, int n_arrays, cons
   p.n = n_arrays;
   p.B = batch;
   p.wait_ns = wait_limit();
-  // Arrays with blocks of 4 KiB and more, in multiples of 16 bytes, go by bulk
-  // copies, ahead of the others: 67 MB of 32 KiB blocks moved in 24 us, against 30 us
-  // by the threads; below that a copy's fixed cost is as large as its bytes'.
+  // Arrays with blocks of 16 KiB and more, in multiples of 16 bytes, go by bulk copies,
+  // ahead of the others: 67 MB of 32 KiB blocks, each read and written, moved in 20.7 us,
+  // against 29.5 by the threads, of 16 KiB blocks in 21.0 against 27.3.  Of 8 KiB blocks
+  // both take 27.5, of 4 KiB blocks the bulk copies 44.7 (a copy has a fixed cost) and
+  // the threads 24.9.
   std::stable_partition(p.a, p.a + p.n, [&](CcArray& c) {
     const int64_t unit = c.item * (c.per_block ? 1 : block);
-    c.parts = c.vec == 16 && unit >= 4096 ? (int)((unit + kCcPiece - 1) / kCcPiece) : 0;
+    c.parts = c.vec == 16 && unit >= 16384 ? (int)((unit + kCcPiece - 1) / kCcPiece) : 0;
     p.n_bulk += c.parts > 0;
     return c.parts > 0;
   });
-  int64_t bytes = 0, pieces = 0;
+  int64_t turn = 0, pieces = 0;
   for (int i = 0; i < p.n; ++i) {
     if (i < p.n_bulk)
       pieces += (int64_t)batch * budget * p.a[i].parts;
     else
-      bytes += p.a[i].item * (p.a[i].per_block ? 1 : block);
+      turn += p.a[i].per;
   }
-  p.group = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(kCcMaxGroup, budget), 32768 / std::max<int64_t>(bytes, 1)));
+  // Entries of a turn: two shares to a warp, or fewer while SMs are idle.  134 MB of rows
+  // of 512 bytes with their accounts and scales, 8 x 16384 of 32768 kept: 25.5 us (5.3
+  // TB/s) with 14 shares to a turn, 32.1 with 8 and 27.8 with 28.
+  p.group = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(kCcMaxGroup, budget), 14 * kCcShare / std::max<int64_t>(turn, 1)));
+  while (p.group > 1 && (int64_t)batch * ((budget + p.group - 1) / p.group) * 2 <= s->num_sms) p.group = (p.group + 1) / 2;
   const int64_t groups = (int64_t)batch * ((budget + p.group - 1) / p.group);
   if (p.n_bulk > 0)
     return cache_launch(cache_compact_bulk_kernel, p, dim3((unsigned)std::min<int64_t>(pieces, s->num_sms)), kCcBulkThreads,
