@@ -189,6 +189,11 @@ __device__ __forceinline__ void aq_swap_queries(uint32_t q, int bytes, int threa
 // The cluster's partial results meet in shared memory: every CTA sends each 32
 // channels x 4 heads of its O^T to the CTA that owns them, and each owner adds
 // the C contributions in rank order, scaled to the common maximum.
+//
+// 128 heads of 512 channels: 8 batch rows over 1024 + 128 rows take 19.6 us, 512 over
+// 2048 rows of one cache 585 us (28% of the measured tensor rate).  What bounds it is
+// the chain within a chunk, and shared memory: the MMAs and the widened rows want half
+// of a chunk's time of its bandwidth.
 constexpr int kAqWorkers = 8;
 constexpr int kAqThreads = (kAqWorkers + 1) * 32;
 
@@ -681,7 +686,8 @@ __global__ void __launch_bounds__(kAqThreads, 1)
 // of a score for every head and row would cost more than the row's own bytes.
 // With a row to a thread the sum over heads never leaves the thread: four
 // threads share a row, their sums and then the CTAs' are added in a fixed order,
-// and each slot's total is added to its account once.
+// and each slot's total is added to its account once.  8 batch rows of 128 heads of 512
+// channels over 1024 rows take 7.7 us, a floor of 0.8: the chain slots, rows, scores.
 constexpr int kAmWorkers = 16;
 constexpr int kAmThreads = (kAmWorkers + 1) * 32;
 constexpr int kAmMaxCluster = 8;

@@ -43,7 +43,7 @@ __device__ __forceinline__ int ce_len(const int32_t* len, int T, int b, int* sta
 // so a digit costs one cluster barrier.  Then each CTA knows how many blocks stay
 // before its share, each thread how many before its own run of blocks, and the
 // list comes out in order.  The bytes (4 per row) are few: what bounds it is the
-// chain of barriers.
+// chain of barriers (4096 rows one by one 8.7 us, 8 x 32768 in blocks of 64 9.3).
 constexpr int kCeThreads = 1024;
 constexpr int kCeMaxCluster = 8;
 constexpr int kCeBins = 2048;
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(256, 3) cache_compact_kernel(const CcParams p)
 // issues, and up to two stores behind it.  The threads of warp 0 work out 32
 // pieces at a time, its first lane issues; the other warps move the small arrays
 // meanwhile.  Each byte that stays is read and written once: what bounds it is the
-// memory's copy rate.
+// memory's copy rate (67 MB of 32 KiB blocks in 20.7 us, 6.5 TB/s read and written).
 constexpr int kCcPiece = 32768;
 constexpr int kCcStages = 6;
 constexpr int kCcAhead = 3;

@@ -249,7 +249,7 @@ extern "C" int ds_sparse_attention_q8(const void* q, const void* codes, int64_t 
   // exchanges partial results; what has the least of both, over all waves of CTAs, is
   // taken.  128 heads over 1024 + 128 rows: one batch row 16 heads, 9 CTAs 10.3 us
   // (64, 10: 17), eight 32, 4 18.4 us (64, 6: 21.5), thirty-two 64, 2 35.0 us (32, 1:
-  // 37.3).  (int8; e4m3 codes, which are checked for NaN, take 2 to 5% more.)
+  // 37.3).  (Before e4m3 codes were checked for NaN, which takes 2 to 5% more.)
   const int G = heads / kv_heads;
   auto turns = [&](int r, int c) { return ((k + r - 1) / r + (W + r - 1) / r + c - 1) / c; };
   int n = 0;
