@@ -406,6 +406,11 @@ int ds_cache_quantize(const void* rows, int64_t rows_batch_stride, int64_t row_s
  * Scales and window rows are expected to be finite; a NaN that is attended (a
  * code, a scale or a window value) makes the outputs of its KV head's query heads
  * NaN.  Rows and scales that no slot names do not matter.
+ * In the weighted sum a weight, times its row's scale, is the sum of two bfloat16
+ * numbers (off by at most 2^-16 of it), so that out is the formula's value rounded
+ * once but for float32 sums.  Calls of more than 64 rows with more than 32 query
+ * heads to a KV head may round it to one (half a step, 2^-8 of it).  The normaliser
+ * and lse are summed from the unrounded weights.
  * Returns DS_OK, DS_ERR_ARG, DS_ERR_UNSUPPORTED or DS_ERR_CUDA.
  */
 int ds_sparse_attention_q8(const void* q, const void* codes, int64_t codes_batch_stride, const float* scales,

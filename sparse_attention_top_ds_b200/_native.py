@@ -688,6 +688,8 @@ def ds_sparse_attention_q8(q, codes, scales, idx, block, scale=None, win=None, w
     win    bf16 [batch, W, kv_heads, d] or None;  win_len  int32 [batch] or None (= W);
     sink   float32 [heads] or None;  scale  default 1/sqrt(d).
     Query head h reads KV head h // (heads // kv_heads).
+    The weights carry 16 bits into the weighted sum, or 8 (bfloat16) in calls of more than
+    64 rows with more than 32 query heads to a KV head.
     Returns out bf16 [batch, heads, d], or (out, lse float32 [batch, heads]).
     """
     if stream is None and out is None and lse is None:

@@ -167,9 +167,20 @@ __device__ __forceinline__ void aq_swap_queries(uint32_t q, int bytes, int threa
 // scale is one factor of a thread and the queries are the narrow operand:
 //     S^T [rows, heads]    = rows . Q^T    (K = channels)
 //     O^T [channels, heads] += rows^T . P^T  (K = rows), P = 2^(z - m) * scale,
-// with S^T (N columns) and O^T (N columns for each 128 channels) in tensor
-// memory: 5 N <= 320 of its 512 columns.  The widened rows serve both products
+// with S^T (N columns) and O^T (N columns for each 128 channels, or 2 N) in tensor
+// memory: at most 320 of its 512 columns.  The widened rows serve both products
 // (128 KiB at 512 channels), the queries stay (64 KiB), P^T takes 16 KiB.
+//
+// A weight times its row's scale is the sum of two bfloat16 numbers, the rounded value
+// and the rounded rest (together off by at most 2^-16 of it), as long as N <= 32: they
+// are 2 N columns of one P^T, an MMA of which takes as long as one of N, and O^T is
+// their two halves' sum.  Rounded once, a weight is off by up to half a bfloat16 step
+// (2^-8 of it); with few attended rows nothing averages that out, and the outputs were
+// up to 1.7 times as far from the exact ones as their own rounding puts them.  With 64
+// heads the second half would not fit tensor memory (576 columns).  A call of at most 64
+// rows leaves half of P^T's 128 rows free: they take the rests, with MMAs of their own.
+// More rows average the roundings out (585 us at 512 tokens over 2048 rows, 1.3 times the
+// distance; such MMAs would add a fifth to a chunk): their weights are rounded once.
 //
 // A chunk passes through in turn: the widened rows serve both products, so
 // nothing of the next chunk can be stored before the weighted sum has freed its
@@ -269,6 +280,11 @@ __device__ __forceinline__ uint32_t aq_pack(float lo, float hi) {
   return u;
 }
 
+// Two weights as bfloat16 numbers, and what they lose as two more.
+__device__ __forceinline__ uint32_t aq_rest(float lo, float hi, uint32_t packed) {
+  return aq_pack(lo - __uint_as_float(packed << 16), hi - __uint_as_float(packed & 0xffff0000u));
+}
+
 __device__ __forceinline__ void dsmem_st_f32x2(uint32_t addr, float x, float y) {
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
@@ -279,11 +295,13 @@ __device__ __forceinline__ void dsmem_st_f32x4(uint32_t addr, const float* v) {
                : "memory");
 }
 
-template <int FMT, int N>
+// FEW (N = 64 only): chunks of at most 64 rows, whose weights' rests are rows 64 and up of P^T.
+template <int FMT, int N, bool FEW>
 __global__ void __launch_bounds__(kAqThreads, 1)
     attn_q8_kernel(const __grid_constant__ CUtensorMap tm_q, const AqParams p) {
   using L_ = AqSmem<N>;
   constexpr int NH = N / 2;  // heads of a softmax thread
+  constexpr int kTerms = N <= 32 ? 2 : 1, NO = kTerms * N;  // columns of O^T for 128 channels
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -298,7 +316,7 @@ __global__ void __launch_bounds__(kAqThreads, 1)
   const int C = p.C, rank = blockIdx.x % C;
   const int G = p.H / p.Hkv, tile = blockIdx.x / C;
   const int ht = tile % p.HT, g = tile / p.HT % p.Hkv, b = tile / p.HT / p.Hkv;
-  constexpr uint32_t kCols = N == 64 ? 512 : N == 32 ? 256 : 128;  // >= 5 N
+  constexpr uint32_t kCols = N == 16 ? 256 : 512;  // >= 4 NO + N
 
   if (tid == 0) {
     for (int i = 0; i < MT; ++i) {
@@ -320,7 +338,7 @@ __global__ void __launch_bounds__(kAqThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot, tmem_st = tmem + (uint32_t)(MT * N);
+  const uint32_t tmem = *tmem_slot, tmem_st = tmem + (uint32_t)(MT * NO);
   pdl_wait();
   pdl_launch_dependents();
 
@@ -452,9 +470,10 @@ __global__ void __launch_bounds__(kAqThreads, 1)
           for (int h = 0; h < NH; ++h) l[h] *= bc[32 + h];
           for (int m = 0; m < MT; ++m) {
 #pragma unroll
-            for (int h = 0; h < NH; h += 8) {
+            for (int j = 0; j < NH * kTerms; j += 8) {
+              const int h = j % NH;  // (the first terms of this thread's heads, then the second)
               uint32_t o[8];
-              const uint32_t at = tmem + lane_base + (uint32_t)(m * N + part * NH + h);
+              const uint32_t at = tmem + lane_base + (uint32_t)(m * NO + j / NH * N + part * NH + h);
               tmem_ld8(at, o);
               tmem_wait_ld();
 #pragma unroll
@@ -472,18 +491,29 @@ __global__ void __launch_bounds__(kAqThreads, 1)
       const uint32_t prow = p_s + (uint32_t)row * 128u, sw7 = (uint32_t)(row & 7);
 #pragma unroll
       for (int h = 0; h < NH; h += 8) {
-        uint32_t u[4];
+        uint32_t u[4], u2[4];
 #pragma unroll
         for (int e = 0; e < 8; e += 4) {
           const float4 mu = *reinterpret_cast<const float4*>(bc + h + e);
           const float e0 = aq_ex2(fmaf(z[h + e], fac, -mu.x)), e1 = aq_ex2(fmaf(z[h + e + 1], fac, -mu.y));
           const float e2 = aq_ex2(fmaf(z[h + e + 2], fac, -mu.z)), e3 = aq_ex2(fmaf(z[h + e + 3], fac, -mu.w));
           l[h + e] += e0, l[h + e + 1] += e1, l[h + e + 2] += e2, l[h + e + 3] += e3;
-          // the weighted sum's operand: the weight times the row's scale, rounded once to bfloat16
+          // the weighted sum's operand: the weight times the row's scale
           u[e / 2] = aq_pack(e0 * rs, e1 * rs);
           u[e / 2 + 1] = aq_pack(e2 * rs, e3 * rs);
+          if constexpr (kTerms == 2 || FEW) {
+            u2[e / 2] = aq_rest(e0 * rs, e1 * rs, u[e / 2]);
+            u2[e / 2 + 1] = aq_rest(e2 * rs, e3 * rs, u[e / 2 + 1]);
+          }
         }
-        sts128(prow + (((uint32_t)((part * NH + h) >> 3) ^ sw7) << 4), make_uint4(u[0], u[1], u[2], u[3]));
+        const uint32_t at = prow + (((uint32_t)((part * NH + h) >> 3) ^ sw7) << 4);
+        if constexpr (kTerms == 2) {
+          sts128(at, make_uint4(u[0], u[1], u[2], u[3]));
+          sts128(prow + (((uint32_t)((N + part * NH + h) >> 3) ^ sw7) << 4), make_uint4(u2[0], u2[1], u2[2], u2[3]));
+        } else if (!FEW || row < 64) {
+          sts128(at, make_uint4(u[0], u[1], u[2], u[3]));
+          if constexpr (FEW) sts128(at + 64u * 128u, make_uint4(u2[0], u2[1], u2[2], u2[3]));
+        }
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -519,7 +549,7 @@ __global__ void __launch_bounds__(kAqThreads, 1)
     }
     aq_wait(mine > 0 ? bar_x : bar_q, 0, p);  // (no copy may be in flight at the end)
     constexpr uint32_t id1 = idesc_bf16_f32(kAqRows, N);
-    constexpr uint32_t id2 = idesc_bf16_f32(128, N) | (1u << 15) | (1u << 16);
+    constexpr uint32_t id2 = idesc_bf16_f32(128, NO) | (1u << 15) | (1u << 16);
     const uint64_t ka = sw128_kmajor_desc(rows_s), kb = sw128_kmajor_desc(q_s);
     const uint64_t ma = sw128_mnmajor_desc(rows_s, kAqBlock, 1024u), mb = sw128_mnmajor_desc(p_s, kAqBlock, 1024u);
     for (int i = 0; i < mine; ++i) {
@@ -546,8 +576,15 @@ __global__ void __launch_bounds__(kAqThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             if (kk < steps)
-              mma_bf16_ss(tmem + (uint32_t)(m * N), desc_at(a0, (uint32_t)(kk * 2048)), desc_at(mb, (uint32_t)(kk * 2048)), id2,
+              mma_bf16_ss(tmem + (uint32_t)(m * NO), desc_at(a0, (uint32_t)(kk * 2048)), desc_at(mb, (uint32_t)(kk * 2048)), id2,
                           (i | kk) != 0 ? 1u : 0u);
+          if constexpr (FEW) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              if (kk < steps)
+                mma_bf16_ss(tmem + (uint32_t)(m * NO), desc_at(a0, (uint32_t)(kk * 2048)),
+                            desc_at(mb, (uint32_t)((kk + 4) * 2048)), id2, 1u);
+          }
           mma_commit(empty0 + 8u * (uint32_t)m);
         }
       }
@@ -569,6 +606,20 @@ __global__ void __launch_bounds__(kAqThreads, 1)
   const int q4 = warp & 3;
   uint16_t* out = p.out + ((size_t)b * p.H + (size_t)g * G) * D;
   const int U = (D >> 5) * (N / 4), per = (U + C - 1) / C;  // pieces of 32 channels x 4 heads; per owner
+  // 16 heads of 32 channels of this CTA's O^T
+  auto sums = [&](int m, int c16, float (&v)[16]) {
+    const uint32_t at = tmem + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(m * NO + c16 * 16);
+    aq_tmem_ld<16>(at, v);
+    if constexpr (kTerms == 2) {
+      float w[16];
+      aq_tmem_ld<16>(at + (uint32_t)N, w);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] += w[e];
+    } else {
+      tmem_wait_ld();
+    }
+  };
   const uint32_t inv_C = (65536u + (uint32_t)C - 1u) / (uint32_t)C;  // u / C = u * inv_C >> 16 for u <= 256
   if (warp == kAqWorkers) {
     for (int h = lane; h < N; h += 32) {
@@ -598,8 +649,7 @@ __global__ void __launch_bounds__(kAqThreads, 1)
       if (m * 128 + q4 * 32 >= D) continue;
       float v[16];
       if (mine > 0) {
-        aq_tmem_ld<16>(tmem + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(m * N + c16 * 16), v);
-        tmem_wait_ld();
+        sums(m, c16, v);
       } else {
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = 0.0f;
@@ -655,8 +705,7 @@ __global__ void __launch_bounds__(kAqThreads, 1)
       if (m * 128 + q4 * 32 >= D) continue;
       float v[16];
       if (mine > 0) {
-        aq_tmem_ld<16>(tmem + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(m * N + c16 * 16), v);
-        tmem_wait_ld();
+        sums(m, c16, v);
       } else {
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = 0.0f;

@@ -44,12 +44,15 @@ static bool cache_encode_q(const void* q, long long rows, int D, int n, CUtensor
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The attention's kernel for n = 16, 32 or 64 heads to a CTA.
+// The attention's kernel for n = 16, 32 or 64 heads to a CTA; few: for calls of at most 64 rows.
 typedef void (*AqKernel)(const CUtensorMap, const AqParams);
-static AqKernel aq_kernel(int dtype, int n) {
-  if (dtype == DS_E4M3)
-    return n == 16 ? attn_q8_kernel<kFmtE4m3, 16> : n == 32 ? attn_q8_kernel<kFmtE4m3, 32> : attn_q8_kernel<kFmtE4m3, 64>;
-  return n == 16 ? attn_q8_kernel<kFmtI8, 16> : n == 32 ? attn_q8_kernel<kFmtI8, 32> : attn_q8_kernel<kFmtI8, 64>;
+template <int FMT>
+static AqKernel aq_kernel_of(int n, bool few) {
+  if (n == 64) return few ? attn_q8_kernel<FMT, 64, true> : attn_q8_kernel<FMT, 64, false>;
+  return n == 16 ? attn_q8_kernel<FMT, 16, false> : attn_q8_kernel<FMT, 32, false>;
+}
+static AqKernel aq_kernel(int dtype, int n, bool few) {
+  return dtype == DS_E4M3 ? aq_kernel_of<kFmtE4m3>(n, few) : aq_kernel_of<kFmtI8>(n, few);
 }
 // Shared memory that a CTA of the attention or the account asks for at least.  Its
 // cluster waits for all its CTAs, and a CTA waits for its tensor memory: two clusters
@@ -97,13 +100,14 @@ static void aq_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int n,
 // clusters of each size of the attention run at once (0: none).
 static cudaError_t cache_setup(DeviceState* s) {
   for (int dtype : {DS_E4M3, DS_I8})
-    for (int n : {16, 32, 64}) {
-      cudaError_t e = cudaFuncSetAttribute(aq_kernel(dtype, n), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           aq_smem(n, DS_ATTN_MAX_DIM));
-      if (e != cudaSuccess) return e;
-      if (cudaFuncSetAttribute(aq_kernel(dtype, n), cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-        cudaGetLastError();
-    }
+    for (int n : {16, 32, 64})
+      for (bool few : {false, true}) {
+        const AqKernel kern = aq_kernel(dtype, n, few);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, aq_smem(n, DS_ATTN_MAX_DIM));
+        if (e != cudaSuccess) return e;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+          cudaGetLastError();
+      }
   for (int dtype : {DS_BF16, DS_E4M3, DS_I8})
     for (int n : {16, 32, 64}) {
       const cudaError_t e = cudaFuncSetAttribute(am_kernel(dtype, n), cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -118,7 +122,7 @@ static cudaError_t cache_setup(DeviceState* s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     aq_config(&cfg, attr, 64, DS_ATTN_MAX_DIM, (unsigned)c, c);
-    if (cudaOccupancyMaxActiveClusters(&s->aq_clusters[c], aq_kernel(DS_E4M3, 64), &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&s->aq_clusters[c], aq_kernel(DS_E4M3, 64, false), &cfg) != cudaSuccess) {
       cudaGetLastError();
       s->aq_clusters[c] = 0;
     }
@@ -274,6 +278,7 @@ extern "C" int ds_sparse_attention_q8(const void* q, const void* codes, int64_t 
   if (tiles * C > INT32_MAX) return DS_ERR_ARG;
   // the fewest rows that keep the number of turns
   for (p.R = kAqRows; p.R > 16 && turns(p.R - 16, C) == turns(kAqRows, C);) p.R -= 16;
+  const bool few = k + W <= 64;  // (then R <= 64: slots and window rows are chunks of their own)
   CUtensorMap tq;
   if (!cache_encode_q(q, (long long)batch * heads, d, n, &tq)) return DS_ERR_ARG;
   cudaLaunchConfig_t cfg = {};
@@ -282,7 +287,7 @@ extern "C" int ds_sparse_attention_q8(const void* q, const void* codes, int64_t 
   cfg.stream = static_cast<cudaStream_t>(stream);
   set_pdl(attr[1]);
   cfg.numAttrs = pdl_on() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, aq_kernel(dtype, n), tq, p) == cudaSuccess ? DS_OK : DS_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, aq_kernel(dtype, n, few), tq, p) == cudaSuccess ? DS_OK : DS_ERR_CUDA;
 }
 
 extern "C" int ds_attention_mass(const void* q, const void* cache, int64_t cache_batch_stride, const float* scales,

@@ -260,6 +260,44 @@ def test_attention_matches_the_oracle(cuda_device, case):
     check_attention(case, a, out, lse)
 
 
+# B, H, K, d, T, k, W, block, fmt, shared, sink, holes, win_len: at most 32 query heads to a KV head, or at most 64 rows
+FEW = [
+    (3, 1, 1, 64, 50, 1, 0, 1, "e4m3", False, False, 0.0, None),
+    (6, 16, 2, 512, 90, 2, 0, 4, "int8", False, False, 0.0, None),
+    (5, 32, 1, 192, 200, 3, 0, 1, "e4m3", False, True, 0.0, None),
+    (4, 64, 2, 320, 120, 7, 2, 1, "int8", True, False, 0.0, [2, 0, 1, 2]),
+    (3, 24, 1, 448, 300, 40, 9, 8, "e4m3", False, True, 0.2, [9, 1, 4]),
+    (2, 32, 1, 512, 600, 150, 70, 2, "e4m3", False, False, 0.0, None),
+    (160, 128, 1, 128, 80, 2, 0, 1, "int8", True, False, 0.0, None),
+    (80, 100, 1, 256, 90, 33, 31, 1, "e4m3", True, True, 0.0, None),
+    (300, 128, 1, 64, 90, 20, 5, 2, "e4m3", True, False, 0.1, None),
+    (250, 33, 1, 512, 70, 64, 0, 1, "int8", True, False, 0.0, None),
+]
+
+
+@pytest.mark.parametrize("case", FEW, ids=lambda c: "x".join(map(str, c[:10])))
+def test_attention_over_few_rows_is_rounded_once(cuda_device, case):
+    """A weight of out is the sum of two bfloat16 numbers, the second rounded from what the first lost: off by at most
+    2^-8 * 2^-8 of it.  So out before its rounding is off by t = (2^-16 + 2 dz + n 2^-23 + 2^-20) spread (the terms of
+    the file's bounds with 2^-16 for the weights' 2^-8), and out by t and half a step at |ref| + t: a bfloat16 number has 8
+    bits, so half a step at y is 2^(floor(log2 y) - 8)."""
+    a = attend_inputs(case)
+    (out, lse), _ = attend(case, a)
+    ok_status(skipped=case[11] > 0)
+    B, H, K, d, T, k, W, block, fmt, shared = case[:10]
+    wide = (np.broadcast_to(a["codes"], (B,) + a["codes"].shape[1:]), np.broadcast_to(a["scales"], (B,) + a["scales"].shape[1:]))
+    ref, ref_lse, spread, reach = oracle.attention_q8(a["q"], *wide, a["idx"], block, fmt, a["scale"], win=a["win"], win_len=a["win_len"],
+                                                sink=a["sink"])
+    t = (2.0 ** -16 + 2 * (d + 8) * 2.0 ** -23 * reach + (k + W) * 2.0 ** -23 + 2.0 ** -20)[..., None] * spread
+    half = np.exp2(np.floor(np.log2(np.maximum(np.abs(ref) + t, 1e-30))) - 8)
+    err = np.abs(dec(bits_of(out)) - ref)
+    assert np.all(err <= t + half), (np.max(err / (t + half)), np.mean(err > t + half))
+    none = np.isneginf(ref_lse)  # no row and no sink
+    assert np.array_equal(np.isneginf(lse.cpu().numpy()), none)
+    tol = ((d + 8) * 2.0 ** -23 + 2.0 ** -22) * reach + (k + W) * 2.0 ** -24 + 2.0 ** -20 * (1 + np.abs(np.where(none, 0.0, ref_lse)))
+    assert np.all(np.abs(lse.cpu().numpy() - ref_lse)[~none] <= tol[~none])
+
+
 def test_attention_skips_everything(cuda_device):
     case = (2, 20, 1, 64, 30, 9, 4, 4, "int8", False, False, 0.0, [0, 0])
     a = attend_inputs(case)
