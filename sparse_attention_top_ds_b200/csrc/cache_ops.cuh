@@ -149,6 +149,34 @@ static int cache_attn_check(const void* q, const void* cache, int64_t cache_batc
 
 }  // namespace dstopk
 
+namespace dstopk {
+
+// The bytes that an array has in each batch row: [at + b * step, at + b * step + bytes),
+// step >= bytes where there is more than one.
+struct CacheSpan {
+  uintptr_t at;
+  int64_t step, bytes;
+};
+
+// Does one array have a byte of the other?  Batch row by batch row, since one may lie
+// in the other's gaps (two halves of one buffer [batch, 2, ...]).
+static bool cache_overlap(const CacheSpan& x, const CacheSpan& y, int batch) {
+  const auto end = [&](const CacheSpan& s) { return s.at + (uintptr_t)((batch - 1) * s.step + s.bytes); };
+  if (end(x) <= y.at || end(y) <= x.at) return false;
+  for (int i = 0, j = 0; i < batch && j < batch;) {
+    const uintptr_t a = x.at + (uintptr_t)(i * x.step), b = y.at + (uintptr_t)(j * y.step);
+    if (a + (uintptr_t)x.bytes <= b)
+      ++i;
+    else if (b + (uintptr_t)y.bytes <= a)
+      ++j;
+    else
+      return true;
+  }
+  return false;
+}
+
+}  // namespace dstopk
+
 extern "C" int ds_cache_quantize(const void* rows, int64_t rows_batch_stride, int64_t row_stride, int batch, int n,
                                  int kv_heads, int d, int dtype, int block, const int32_t* pos, const int32_t* len,
                                  void* codes, int64_t codes_batch_stride, float* scales, int64_t scales_batch_stride,
@@ -399,7 +427,7 @@ extern "C" int ds_cache_compact(const ds_cache_array* arrays, int n_arrays, cons
   if (budget < 1 || budget > nb || cache_misaligned(kept, 4) || cache_misaligned(len, 4)) return DS_ERR_ARG;
   if ((int64_t)batch * budget > INT32_MAX) return DS_ERR_ARG;
   CcParams p = {};
-  std::pair<uintptr_t, uintptr_t> src[DS_CACHE_MAX_ARRAYS], dst[DS_CACHE_MAX_ARRAYS];
+  CacheSpan src[DS_CACHE_MAX_ARRAYS], dst[DS_CACHE_MAX_ARRAYS];
   for (int i = 0; i < n_arrays; ++i) {
     const ds_cache_array& a = arrays[i];
     if (!a.src || !a.dst || a.item_bytes < 1 || a.item_bytes > (int64_t(1) << 24) || (a.per_block != 0 && a.per_block != 1))
@@ -408,8 +436,8 @@ extern "C" int ds_cache_compact(const ds_cache_array* arrays, int n_arrays, cons
     const int64_t dst_bytes = a.item_bytes * (a.per_block ? budget : std::min<int64_t>(T, (int64_t)budget * block));
     if (batch > 1 && (a.src_batch_stride < src_bytes || a.dst_batch_stride < dst_bytes)) return DS_ERR_ARG;
     const uintptr_t s0 = reinterpret_cast<uintptr_t>(a.src), d0 = reinterpret_cast<uintptr_t>(a.dst);
-    src[i] = {s0, s0 + (uintptr_t)((batch - 1) * a.src_batch_stride + src_bytes)};
-    dst[i] = {d0, d0 + (uintptr_t)((batch - 1) * a.dst_batch_stride + dst_bytes)};
+    src[i] = {s0, a.src_batch_stride, src_bytes};
+    dst[i] = {d0, a.dst_batch_stride, dst_bytes};
     const uint64_t bits = (uint64_t)s0 | d0 | (uint64_t)a.item_bytes |
                           (batch > 1 ? (uint64_t)a.src_batch_stride | (uint64_t)a.dst_batch_stride : 0);
     CcArray& c = p.a[i];
@@ -426,7 +454,7 @@ extern "C" int ds_cache_compact(const ds_cache_array* arrays, int n_arrays, cons
   // the moves are not ordered among themselves, so no array may be written where one is read
   for (int i = 0; i < n_arrays; ++i)
     for (int j = 0; j < n_arrays; ++j)
-      if (src[i].first < dst[j].second && dst[j].first < src[i].second) return DS_ERR_ARG;
+      if (cache_overlap(src[i], dst[j], batch)) return DS_ERR_ARG;
   DeviceState* s = nullptr;
   const int rc = device_state(&s);
   if (rc != DS_OK) return rc;

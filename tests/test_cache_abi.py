@@ -101,6 +101,39 @@ def test_compact_refuses_an_array_written_where_another_is_read(lib):
         assert call(first, second) == call(second, first) == ds.DS_ERR_ARG, second
 
 
+def compact_two_rows(lib, src, dst, src_step, dst_step, batch=2):
+    """Two batch rows (or more) of 100 items of 1024 bytes, 4 blocks of 16 kept."""
+    arr = struct.pack(_native._CACHE_ARRAY, src, dst, src_step, dst_step, 1024, 0)
+    return lib.ds_cache_compact(arr, 1, A, 4, None, batch, 100, 16, None)
+
+
+SRC, DST = 100 * 1024, 64 * 1024  # bytes of a batch row that are read, and written
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="an accepted call would run on addresses that are none")
+@pytest.mark.parametrize("at,src_step,dst_step", [
+    (SRC, 2 * SRC, 2 * SRC),                 # two halves of a buffer [batch, 2, ...]
+    (-DST, SRC + DST, SRC + DST),            # dst in front of src in each batch row
+    (SRC, SRC + DST, SRC + DST),             # no byte between them
+    (SRC + 16, 5 * SRC, 3 * SRC),            # different strides that never meet
+    (3 * SRC, 2 * SRC, 2 * SRC),             # dst of batch row 0 behind src of batch row 1
+])
+def test_compact_takes_a_dst_in_the_gaps_of_a_src(lib, at, src_step, dst_step):
+    # without a GPU, a call whose arguments are accepted ends at the device
+    assert compact_two_rows(lib, 0x4000000, 0x4000000 + at, src_step, dst_step) not in (ds.DS_ERR_ARG, ds.DS_OK)
+
+
+@pytest.mark.parametrize("at,src_step,dst_step,batch", [
+    (SRC - 1024, 2 * SRC, 2 * SRC, 2),       # two halves, dst one item early
+    (2 * SRC - DST + 1024, 2 * SRC, 2 * SRC, 2),  # and so late that it reaches the next batch row
+    (SRC, SRC + DST - 16, SRC + DST - 16, 2),
+    (SRC, 4 * SRC, 3 * SRC, 3),              # meets in the last batch row only
+    (-DST, 2 * SRC, SRC, 2),                 # dst of batch row 1 within src of batch row 0
+])
+def test_compact_refuses_a_dst_that_meets_a_src_in_some_batch_row(lib, at, src_step, dst_step, batch):
+    assert compact_two_rows(lib, 0x4000000, 0x4000000 + at, src_step, dst_step, batch) == ds.DS_ERR_ARG
+
+
 def test_build_makes_the_front_extension(lib):
     from sparse_attention_top_ds_b200 import build
     assert not build.front_stale()

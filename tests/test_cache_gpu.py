@@ -717,6 +717,25 @@ def test_compact_any_list_stays_inside(cuda_device):
     assert back[0].tolist() == [4, 5, 6, 7, 4, 5, 6, 7, 0, 1] + [-5] * 6
 
 
+@pytest.mark.parametrize("block,width", [(4, 64), (64, 512)])
+def test_compact_from_one_half_of_a_buffer_to_the_other(cuda_device, block, width):
+    # src and dst by turns in one buffer [batch, 2, ...]: they share no byte, although their ranges of addresses meet.
+    # Blocks of 256 bytes move by threads, of 32 KiB by bulk copies
+    B, nb = 3, 7
+    T = nb * block - 1
+    g = np.random.default_rng(block)
+    x = g.integers(0, 256, size=(B, 2, T, width)).astype(np.uint8)
+    m = inputs.accounts(600 + block, B, T)
+    kept, _ = oracle.evict(m, [T] * B, block, 4, 1, 1)
+    for way in (0, 1):
+        buf = torch.from_numpy(x).cuda()
+        ds.ds_cache_compact(i32_to_device(kept), block=block, rows=[(buf[:, way], buf[:, 1 - way])])
+        ok_status()
+        want = x.copy()
+        want[:, 1 - way] = oracle.compact(x[:, way], x[:, 1 - way], kept, [T] * B, block, 0)
+        assert np.array_equal(buf.cpu().numpy(), want)
+
+
 # ---------------------------------------------------------------- refusals of the front end
 
 def test_front_end_refusals(cuda_device):
