@@ -498,8 +498,9 @@ typedef struct {
  *          int32 [batch] or NULL (= T); T 1 .. 16777216 rows of every src.
  * Batch strides, if batch > 1, are at least the bytes of a batch row: src T
  * items (ceil(T / block) with per_block), dst min(T, budget * block) (budget).
- * No byte of an array's dst may be one of an array's src, in any batch rows
- * (DS_ERR_ARG); a dst in the gaps between a src's batch rows may be.
+ * No byte of an array's dst may be one of an array's src, or of another array's
+ * dst, in any batch rows (DS_ERR_ARG); arrays in the gaps between another's batch
+ * rows may be.
  * Returns DS_OK, DS_ERR_ARG, DS_ERR_UNSUPPORTED or DS_ERR_CUDA.
  */
 int ds_cache_compact(const ds_cache_array* arrays, int n_arrays, const int32_t* kept, int budget, const int32_t* len,

@@ -814,9 +814,9 @@ def ds_cache_compact(kept, block=1, length=None, rows=(), blocks=(), stream=None
     blocks  pairs with one entry for each block, [batch, ceil(T / block), ...] and
             [batch, at least budget, ...] (scales).
     The arrays are contiguous behind the batch; a pair has one dtype and trailing
-    shape, and no dst has a byte of a src (two halves of one buffer may be src and
-    dst: buf[:, 0] and buf[:, 1]).  Rows of dst behind what stays are left
-    as they were.
+    shape, and no dst has a byte of a src or of another dst (two halves of one buffer
+    may be src and dst: buf[:, 0] and buf[:, 1]).  Rows of dst behind what stays are
+    left as they were.
     """
     if stream is None and (_front or _load_front()).compact(kept, block, length, rows, blocks):
         return

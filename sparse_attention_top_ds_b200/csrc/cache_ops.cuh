@@ -451,10 +451,11 @@ extern "C" int ds_cache_compact(const ds_cache_array* arrays, int n_arrays, cons
     c.row_per = (uint32_t)(c.item / c.vec);
     c.per = (uint32_t)(a.per_block ? 1 : block) * c.row_per;
   }
-  // the moves are not ordered among themselves, so no array may be written where one is read
+  // the moves are not ordered among themselves, so no array may be written where one is
+  // read, or where another is written
   for (int i = 0; i < n_arrays; ++i)
     for (int j = 0; j < n_arrays; ++j)
-      if (cache_overlap(src[i], dst[j], batch)) return DS_ERR_ARG;
+      if (cache_overlap(src[i], dst[j], batch) || (i < j && cache_overlap(dst[i], dst[j], batch))) return DS_ERR_ARG;
   DeviceState* s = nullptr;
   const int rc = device_state(&s);
   if (rc != DS_OK) return rc;

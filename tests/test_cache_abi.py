@@ -134,6 +134,33 @@ def test_compact_refuses_a_dst_that_meets_a_src_in_some_batch_row(lib, at, src_s
     assert compact_two_rows(lib, 0x4000000, 0x4000000 + at, src_step, dst_step, batch) == ds.DS_ERR_ARG
 
 
+def compact_two_arrays(lib, a, b, batch=2):
+    """Arrays (src, dst, their batch strides, bytes of an item, per_block) of 100 rows in blocks of 16, 4 of them kept."""
+    arr = struct.pack(_native._CACHE_ARRAY * 2, *a, *b)
+    return lib.ds_cache_compact(arr, 2, A, 4, None, batch, 100, 16, None)
+
+
+@pytest.mark.parametrize("dst,step,item,per_block", [
+    (0x8000000, 2 * DST, 1024, 0),           # the same
+    (0x8000000 + DST - 1024, 2 * DST, 1024, 0),
+    (0x8000000 - 4 + 1, 4, 1, 1),            # four bytes a batch row, of the first array's only the first
+    (0x8000000 + 3 * DST - 1, DST, 1, 1),    # of its batch row 1 only
+])
+def test_compact_refuses_two_arrays_written_to_one_place(lib, dst, step, item, per_block):
+    first = (0x4000000, 0x8000000, SRC, 2 * DST, 1024, 0)
+    second = (0x1000000, dst, SRC, step, item, per_block)
+    assert compact_two_arrays(lib, first, second) == compact_two_arrays(lib, second, first) == ds.DS_ERR_ARG
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="an accepted call would run on addresses that are none")
+def test_compact_takes_two_arrays_written_side_by_side(lib):
+    first = (0x4000000, 0x8000000, SRC, 2 * DST, 1024, 0)
+    for second in ((0x1000000, 0x8000000 + DST, SRC, 2 * DST, 1024, 0), (0x1000000, 0x8000000 + 3 * DST, SRC, 4, 1, 1),
+                   (0x4000000, 0x9000000, SRC, DST, 1024, 0)):  # one array, to two places
+        for arrays in ((first, second), (second, first)):
+            assert compact_two_arrays(lib, *arrays) not in (ds.DS_ERR_ARG, ds.DS_OK), second
+
+
 def test_build_makes_the_front_extension(lib):
     from sparse_attention_top_ds_b200 import build
     assert not build.front_stale()
