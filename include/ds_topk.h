@@ -452,7 +452,9 @@ int ds_attention_mass(const void* q, const void* cache, int64_t cache_batch_stri
  *
  * Batch row b holds L = min(max(len[b], 0), T) rows in ceil(L / block) blocks,
  * the last of them perhaps not full.  A block's key is the sum of its rows'
- * accounts, in float64, rounded once to float32.  At most `budget` blocks stay:
+ * accounts, in float64, rounded once to float32: rows 32 apart are added first, in
+ * ascending order, then the sums half of min(block, 32) apart, a quarter, and so on
+ * (rows past L count 0).  At most `budget` blocks stay:
  * the first keep_first and the last keep_last, then those with the largest
  * keys; equal keys go to the lower block, -0.0 equals +0.0, a NaN ranks above
  * +inf.  (A block, not a row, is what leaves: its rows share a scale.)

@@ -3,9 +3,10 @@
 // buffer.
 //
 // For batch row b with L rows in ceil(L / block) blocks, the key of a block is
-// the sum of its valid rows' accounts.  The sum is taken in float64 and rounded
-// once to float32, so that blocks next to the border do not change sides with
-// the order of a sum.  What stays: the first keep_first and the last keep_last
+// the sum of its valid rows' accounts.  The sum is taken in float64, in one order
+// for every block, and rounded once to float32: a key is a function of the block's
+// accounts alone, and another order of the sum could change it only where float64
+// loses digits (terms of both signs that cancel, or more than 2^29 apart).  What stays: the first keep_first and the last keep_last
 // blocks, then the blocks with the largest keys, up to `budget` in all; equal
 // keys go to the lower index, -0.0 equals +0.0, and a NaN ranks above +inf.
 #pragma once
@@ -59,11 +60,29 @@ __device__ __forceinline__ uint32_t ce_order(double sum) {
 
 __device__ __forceinline__ bool ce_protected(const CeParams& p, int n, int nb) { return n < p.first || n >= nb - p.last; }
 
-// The key of block n, by one thread.
+// The key of block n, by one thread, added up in the order of ce_keys: rows half a
+// block apart first, then those sums a quarter apart, and so on.  Taken from the leaves
+// up, the rows come in the order of their reversed bits, and part[l] holds the sum of 2^l
+// of them that waits for its other half.  (Blocks of up to 32 rows only: of longer ones a
+// row has no more than a CTA's keys.)
+static_assert((1 << 24) / kCeMaxCluster / 64 <= kCeKeys, "keys worked out by one thread");
 __device__ __forceinline__ uint32_t ce_key(const CeParams& p, const float* mass, int n, int nb, int L) {
   if (ce_protected(p, n, nb)) return 0xffffffffu;
-  double sum = 0.0;
-  for (int r = n * p.block, r1 = min(L, r + p.block); r < r1; ++r) sum += (double)__ldcg(mass + r);
+  const int log = 31 - __clz(p.block);
+  double part[6], sum = 0.0;
+  for (int i = 0; i < p.block; ++i) {
+    const int r = n * p.block + (int)(log > 0 ? __brev((uint32_t)i) >> (32 - log) : 0u);
+    sum = r < L ? (double)__ldcg(mass + r) : 0.0;
+    bool waits = false;
+#pragma unroll
+    for (int l = 0; l < 6; ++l) {
+      if (waits) continue;
+      if ((i >> l) & 1)
+        sum += part[l];
+      else
+        part[l] = sum, waits = true;
+    }
+  }
   return ce_order(sum);
 }
 
@@ -90,7 +109,8 @@ __device__ __forceinline__ uint2 dsmem_ld_u32x2(uint32_t addr) {
   return v;
 }
 
-// The keys of blocks n0 .. n0 + held - 1: a warp reads 32 rows at a time, min(block,
+// The keys of blocks n0 .. n0 + held - 1, added up in a fixed order (see ce_key; rows 32
+// and more apart first of all): a warp reads 32 rows at a time, min(block,
 // 32) lanes to a block and STEPS reads to each, with 8 reads in flight.
 template <int STEPS>
 __device__ __forceinline__ void ce_keys(const CeParams& p, const float* mass, uint32_t* keys, int n0, int held, int nb, int L) {

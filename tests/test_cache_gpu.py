@@ -605,6 +605,29 @@ def test_evict_long_rows(cuda_device, T, block, budget):
     assert torch.equal(kept.long(), want) and n.tolist() == [budget * block - (nb * block - T)] * 2
 
 
+@pytest.mark.parametrize("block", [4, 8, 16, 32])
+def test_evict_keys_of_equal_blocks_are_equal_wherever_they_are(cuda_device, block):
+    # More blocks to a CTA than it holds keys of, made of a few patterns of accounts that cancel, so that a sum in another
+    # order is another: blocks of one pattern have one key, and the lower ones stay.  The keys: halves of a block added row
+    # by row, then halves of that.
+    nb = 8 * 48 * 1024 + 90_001
+    g = torch.Generator("cuda").manual_seed(block)
+    pool = torch.rand(8, block, device="cuda", generator=g) + 0.5
+    for i, at in enumerate((0, 0, 1, 1, 0, 1, 0, 1)):  # a large term that cancels some rows later
+        pool[i, at], pool[i, block // 2 + (i * 5 + at) % (block // 2)] = 1e25, -1e25
+    pick = torch.randint(0, 8, (1, nb), device="cuda", generator=g)
+    m = pool[pick].view(1, nb * block)
+    x = pool.double()
+    while x.shape[1] > 1:
+        x = x[:, :x.shape[1] // 2] + x[:, x.shape[1] // 2:]
+    key = x[:, 0].float()[pick]
+    budget = nb // 3
+    kept, n = ds.ds_cache_evict(m, budget, block=block, keep_last=0)
+    ok_status()
+    want = key.sort(dim=1, descending=True, stable=True).indices[:, :budget].sort(dim=1).values
+    assert torch.equal(kept.long(), want) and n.tolist() == [budget * block]
+
+
 @pytest.mark.parametrize("kind", ["tail", "ties", "zeros", "special"])
 @pytest.mark.parametrize("case", EVICT, ids=lambda c: "x".join(map(str, c[:6])))
 def test_evict_matches_the_oracle(cuda_device, case, kind):
