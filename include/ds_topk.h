@@ -536,13 +536,19 @@ int ds_set_wait_limit(int64_t ns);
 
 /*
  * ds_plant_wait_fault -- testing the failure detection: the next `launches`
- * indexer scorer launches (of ds_indexer_score, ds_indexer_topk and its
- * variants) each carry a planted fault: in their first CTA one epilogue warp
- * skips its first release of a tensor-core accumulator, so that the MMA warp's
- * wait for that accumulator, and the waits behind it, run out after the wait
- * limit.  The kernel then scores that CTA's remaining positions as -inf, lets
- * its copies in flight land, frees its tensor memory and returns; the call's
- * status is DS_ERR_TIMEOUT.  0 disarms.  launches >= 0, else DS_ERR_ARG.
+ * launches of the kernels named here each carry a planted fault, and the call's
+ * status is DS_ERR_TIMEOUT:
+ *  - the indexer scorer (of ds_indexer_score, ds_indexer_topk and its variants):
+ *    in its first CTA one epilogue warp skips its first release of a tensor-core
+ *    accumulator, so that the MMA warp's wait for that accumulator, and the waits
+ *    behind it, run out after the wait limit.  The kernel then scores that CTA's
+ *    remaining positions as -inf, lets its copies in flight land, frees its tensor
+ *    memory and returns;
+ *  - the copy kernel of ds_cache_compact (arrays with blocks of 16 KiB and more): its
+ *    first CTA does not announce its first load, so that the wait for it runs out.
+ *    The CTA starts no further load, lets those in flight land and returns; what it had
+ *    not stored stays as it was.
+ * 0 disarms.  launches >= 0, else DS_ERR_ARG.
  * Nothing traps, and the next call without the fault runs normally.  A
  * launch captured into a CUDA graph keeps the fault it was captured with.
  * (No counterpart on the pages.)

@@ -286,6 +286,7 @@ struct CcParams {
   int n_bulk;           // the first n_bulk arrays go by bulk copies
   int B;
   uint64_t wait_ns;
+  int fault;            // testing the failure detection: 1 = CTA 0's first load is not announced to its barrier
 };
 
 // Where an entry comes from: its block and the block's valid rows, or -1 and 0.
@@ -423,7 +424,8 @@ __global__ void __launch_bounds__(kCcBulkThreads, 1) cache_compact_bulk_kernel(c
     bytes = n < 0 || have <= 0 ? 0u : (uint32_t)min(have, (long long)kCcPiece);
   };
   bool ok = true;
-  for (int s = -kCcAhead; s < mine; ++s) {
+  int s = -kCcAhead;
+  for (; ok && s < mine; ++s) {
     const int ld = s + kCcAhead;
     if (ld < mine) {
       if ((ld & 31) == 0) {
@@ -435,9 +437,9 @@ __global__ void __launch_bounds__(kCcBulkThreads, 1) cache_compact_bulk_kernel(c
       if (lane == 0) {
         // the store before last of this stage has read it
         asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kCcStages - 1 - kCcAhead) : "memory");
-        if (ok && n > 0) {
+        if (n > 0) {
           const uint32_t bar = smem_u32(bars + ld % kCcStages);
-          mbar_arrive_expect_tx(bar, n);
+          if (p.fault == 0 || blockIdx.x != 0 || ld != 0) mbar_arrive_expect_tx(bar, n);
           bulk_g2s(ring + (uint32_t)(ld % kCcStages) * kCcPiece, at, n, bar);
         } else {
           mbar_arrive(smem_u32(bars + ld % kCcStages));
@@ -450,13 +452,19 @@ __global__ void __launch_bounds__(kCcBulkThreads, 1) cache_compact_bulk_kernel(c
       uint8_t* at = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)(old ? dst_held : dst), s & 31));
       const uint32_t n = __shfl_sync(0xffffffffu, old ? bytes_held : bytes, s & 31);
       if (lane == 0) {
-        ok = mbar_wait_bounded(smem_u32(bars + s % kCcStages), (uint32_t)((s / kCcStages) & 1), p.status, p.wait_ns) && ok;
+        ok = mbar_wait_bounded(smem_u32(bars + s % kCcStages), (uint32_t)((s / kCcStages) & 1), p.status, p.wait_ns);
         if (ok && n > 0) bulk_s2g(at, ring + (uint32_t)(s % kCcStages) * kCcPiece, n);
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
     __syncwarp();
   }
+  // After a wait that ran out (on piece s - 1) the loads that were issued still land in
+  // this CTA's memory: each is waited for once more before the memory is given back.
+  if (!ok && lane == 0)
+    for (int i = s - 1; i < min(s + kCcAhead, mine); ++i)
+      mbar_wait_bounded(smem_u32(bars + i % kCcStages), (uint32_t)((i / kCcStages) & 1), p.status, p.wait_ns);
   if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 

@@ -492,8 +492,10 @@ extern "C" int ds_cache_compact(const ds_cache_array* arrays, int n_arrays, cons
   p.group = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(kCcMaxGroup, budget), 14 * kCcShare / std::max<int64_t>(turn, 1)));
   while (p.group > 1 && (int64_t)batch * ((budget + p.group - 1) / p.group) * 2 <= s->num_sms) p.group = (p.group + 1) / 2;
   const int64_t groups = (int64_t)batch * ((budget + p.group - 1) / p.group);
-  if (p.n_bulk > 0)
+  if (p.n_bulk > 0) {
+    p.fault = take_planted_fault();
     return cache_launch(cache_compact_bulk_kernel, p, dim3((unsigned)std::min<int64_t>(pieces, s->num_sms)), kCcBulkThreads,
                         kCcSmem, stream);
+  }
   return cache_launch(cache_compact_kernel, p, dim3((unsigned)std::min<int64_t>(groups, 1 << 20)), 256, 0, stream);
 }

@@ -51,8 +51,8 @@ static std::mutex g_mu;
 static DeviceState g_dev[kMaxDevices];
 
 // Limit of the kernels' bounded waits, in ns (0: kWaitLimitNs), read at each
-// launch; and the number of scorer launches still to carry the planted fault
-// that makes one of their waits run out (testing the failure detection).
+// launch; and the number of launches still to carry the planted fault that makes
+// one of their waits run out (testing the failure detection).
 static std::atomic<long long> g_wait_ns{0};
 static std::atomic<int> g_planted{0};
 
