@@ -544,6 +544,10 @@ int ds_set_wait_limit(int64_t ns);
  *    behind it, run out after the wait limit.  The kernel then scores that CTA's
  *    remaining positions as -inf, lets its copies in flight land, frees its tensor
  *    memory and returns;
+ *  - ds_sparse_attention_q8 and ds_attention_mass: in their first CTA the MMA warp
+ *    awaits an arrival on the rows that does not come.  The CTA's waits end within
+ *    about one limit; MMAs and copies in flight end, tensor memory is freed.  The
+ *    attention's outputs then mean nothing; that CTA's weights go to no account;
  *  - the copy kernel of ds_cache_compact (arrays with blocks of 16 KiB and more): its
  *    first CTA does not announce its first load, so that the wait for it runs out.
  *    The CTA starts no further load, lets those in flight land and returns; what it had

@@ -169,9 +169,9 @@ def ds_set_wait_limit(ns):
 
 
 def ds_plant_wait_fault(launches):
-    """Testing the failure detection: the next `launches` launches of the scorer and
-    the copy kernel of ds_cache_compact each make one of their bounded waits run out
-    (DS_ERR_TIMEOUT in the status)."""
+    """Testing the failure detection: the next `launches` launches of the scorer,
+    the 8-bit cache's attention and account and the copy kernel of ds_cache_compact
+    each make one of their bounded waits run out (DS_ERR_TIMEOUT in the status)."""
     _check(load().ds_plant_wait_fault(int(launches)), "ds_plant_wait_fault")
 
 

@@ -38,6 +38,7 @@ struct AqParams {
   int T, k, W, B, H, Hkv, D, log_block;
   int HT, R, C;            // head tiles of a KV head, rows of a chunk, CTAs of a cluster
   float scale_log2;        // scale * log2(e)
+  int fault;               // testing the failure detection: 1 = in CTA 0 the rows' barriers await an arrival more than come
 };
 
 __device__ __forceinline__ int aq_window(const AqParams& p, int b) {
@@ -58,11 +59,58 @@ __device__ __forceinline__ float aq_scale(const AqParams& p, int b, int r, int g
   return p.scales[b * p.scales_bstride + (long long)(r >> p.log_block) * p.Hkv + g];
 }
 
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// The wait for an mbarrier that is not there yet.  One that runs out records the timeout and
+// sets the word at gave_up in shared memory, after which the CTA's other waits no longer
+// last: its warps pass all their barriers and the CTA ends within about one limit.  (The
+// attention's outputs then mean nothing.)  What is then still in flight, aq_drain waits
+// for.
+__device__ __forceinline__ void aq_poll(uint32_t bar, uint32_t parity, int* status, uint64_t limit, uint32_t gave_up) {
+  if (limit == 0) limit = kWaitLimitNs;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) break;
+    if ((it & 255u) == 0 && (globaltimer_ns() - t0 > limit || lds32(gave_up) != 0u)) {
+      record_status(status, kErrTimeout);
+      asm volatile("st.shared.u32 [%0], 1;" ::"r"(gave_up) : "memory");
+      break;
+    }
+  }
+}
+static __device__ __noinline__ void aq_poll_far(uint32_t bar, uint32_t parity, int* status, uint64_t limit, uint32_t gave_up) {
+  aq_poll(bar, parity, status, limit, gave_up);
+}
+
 // A warp's wait.  All lanes poll: a chunk's turn is a chain of a dozen such waits,
 // and a wait by one lane with the others behind it woke up later each time (the
-// decode call took 20.5 us instead of 19.0).
-__device__ __forceinline__ void aq_wait(uint32_t bar, uint32_t parity, const AqParams& p) {
-  mbar_wait_bounded(bar, parity, p.status, p.wait_ns);
+// decode call took 20.5 us instead of 19.0).  FAR: the polling is a call, which keeps
+// the code short (8 decode rows 18.8 us, 19.5 polling in place), where what is live fits
+// the registers that a call leaves alone (the workers' of 64 heads do not: 512 tokens over
+// 2048 rows 601 us, 596 in place; nor does it help the account: 879 and 837 on the same).
+template <bool FAR>
+__device__ __forceinline__ void aq_wait(uint32_t bar, uint32_t parity, const AqParams& p, uint32_t gave_up) {
+  if (!mbar_try_wait(bar, parity)) {
+    if constexpr (FAR)
+      aq_poll_far(bar, parity, p.status, p.wait_ns, gave_up);
+    else
+      aq_poll(bar, parity, p.status, p.wait_ns, gave_up);
+  }
+  __syncwarp();
+}
+
+// The end of a CTA that gave up, by the warp that issues: its MMAs and its last copy of
+// queries (announced on bar_q in phase `parity`) are waited for once more, within the
+// limit, before tensor and shared memory are given back.  `bar` has had no use before.
+__device__ __forceinline__ void aq_drain(uint32_t bar, uint32_t bar_q, uint32_t parity, const AqParams& p) {
+  if (elect_lane()) mma_commit(bar);
+  __syncwarp();
+  mbar_wait_bounded(bar, 0, p.status, p.wait_ns);
+  mbar_wait_bounded(bar_q, parity, p.status, p.wait_ns);
   __syncwarp();
 }
 
@@ -310,7 +358,8 @@ __global__ void __launch_bounds__(kAqThreads, 1)
   float2* st = reinterpret_cast<float2*>(smem + L_::st_off(D));
   float* ft = reinterpret_cast<float*>(smem + L_::ft_off(D));
   const uint32_t full0 = sbase + L_::bar_off(D), empty0 = full0 + 32u;  // pairs of blocks: stored [4], summed [4]
-  const uint32_t bar_q = empty0 + 32u, bar_s = bar_q + 8u, bar_p = bar_s + 8u, bar_x = bar_p + 8u;
+  const uint32_t bar_q = empty0 + 32u, bar_s = bar_q + 8u, bar_p = bar_s + 8u, bar_x = bar_p + 8u, bar_d = bar_x + 8u;
+  const uint32_t gave_up = full0 + 16u * 8u + 4u;  // behind the address of tensor memory
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L_::slot_off(D));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = p.C, rank = blockIdx.x % C;
@@ -320,13 +369,15 @@ __global__ void __launch_bounds__(kAqThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < MT; ++i) {
-      mbar_init(full0 + 8u * i, kAqWorkers);
+      mbar_init(full0 + 8u * i, kAqWorkers + (p.fault != 0 && blockIdx.x == 0 ? 1u : 0u));
       mbar_init(empty0 + 8u * i, 1);
     }
     mbar_init(bar_q, 1);
     mbar_init(bar_s, 1);
     mbar_init(bar_p, kAqWorkers);
     mbar_init(bar_x, kAqWorkers);  // queries reordered
+    mbar_init(bar_d, 1);           // the end of a CTA that gave up
+    tmem_slot[1] = 0u;             // gave_up
     fence_mbar_init();
   }
   if (warp == kAqWorkers) {
@@ -415,7 +466,7 @@ __global__ void __launch_bounds__(kAqThreads, 1)
       uint4 w[8];
       fetch(w, c.win, 1);
       if (i == 0) {  // while the first rows are on their way
-        aq_wait(bar_q, 0, p);
+        aq_wait<(N < 64)>(bar_q, 0, p, gave_up);
         aq_swap_queries(q_s, DB * N * 128, tid, kAqWorkers * 32);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_x);
@@ -423,7 +474,7 @@ __global__ void __launch_bounds__(kAqThreads, 1)
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         if (m >= MT) break;
-        if (i > 0) aq_wait(empty0 + 8u * (uint32_t)m, (uint32_t)((i - 1) & 1), p);
+        if (i > 0) aq_wait<(N < 64)>(empty0 + 8u * (uint32_t)m, (uint32_t)((i - 1) & 1), p, gave_up);
         if (c.win) {
           aq_store<kFmtBf16, 2>((m & 1) ? w : v, m, c.n, DB, rows_s);
           if (m < 2) aq_load<kFmtBf16, 2>((m & 1) ? w : v, src, m + 2, DB);
@@ -444,7 +495,7 @@ __global__ void __launch_bounds__(kAqThreads, 1)
       }
       // ---- softmax of chunk i
       const float fac = r >= 0 ? rs * p.scale_log2 : 1.0f;
-      aq_wait(bar_s, (uint32_t)(i & 1), p);
+      aq_wait<(N < 64)>(bar_s, (uint32_t)(i & 1), p, gave_up);
       tc_fence_after();
       float z[NH];
       aq_tmem_ld<NH>(tmem_st + lane_base + (uint32_t)(part * NH), z);
@@ -535,7 +586,7 @@ __global__ void __launch_bounds__(kAqThreads, 1)
     }
     __syncwarp();
     if (mine > 0) {
-      aq_wait(empty0 + 8u * (uint32_t)(MT - 1), (uint32_t)((mine - 1) & 1), p);
+      aq_wait<(N < 64)>(empty0 + 8u * (uint32_t)(MT - 1), (uint32_t)((mine - 1) & 1), p, gave_up);
       tc_fence_after();
     }
   } else {
@@ -547,7 +598,7 @@ __global__ void __launch_bounds__(kAqThreads, 1)
       mbar_arrive_expect_tx(bar_q, (uint32_t)(DB * N * 128));
       tma_load_3d(q_s, &tm_q, 0, b * p.H + g * G + ht * N, 0, bar_q);
     }
-    aq_wait(mine > 0 ? bar_x : bar_q, 0, p);  // (no copy may be in flight at the end)
+    aq_wait<true>(mine > 0 ? bar_x : bar_q, 0, p, gave_up);  // (no copy may be in flight at the end)
     constexpr uint32_t id1 = idesc_bf16_f32(kAqRows, N);
     constexpr uint32_t id2 = idesc_bf16_f32(128, NO) | (1u << 15) | (1u << 16);
     const uint64_t ka = sw128_kmajor_desc(rows_s), kb = sw128_kmajor_desc(q_s);
@@ -555,7 +606,7 @@ __global__ void __launch_bounds__(kAqThreads, 1)
     for (int i = 0; i < mine; ++i) {
       const int steps = (chunk(i).n + 15) >> 4;
       for (int m = 0; m < MT; ++m) {
-        aq_wait(full0 + 8u * (uint32_t)m, (uint32_t)(i & 1), p);
+        aq_wait<true>(full0 + 8u * (uint32_t)m, (uint32_t)(i & 1), p, gave_up);
         tc_fence_after();
         if (elect_lane()) {
           const uint64_t a0 = desc_at(ka, (uint32_t)m * 2 * kAqBlock), b0 = desc_at(kb, (uint32_t)m * 2 * N * 128);
@@ -568,7 +619,7 @@ __global__ void __launch_bounds__(kAqThreads, 1)
         }
         __syncwarp();
       }
-      aq_wait(bar_p, (uint32_t)(i & 1), p);
+      aq_wait<true>(bar_p, (uint32_t)(i & 1), p, gave_up);
       tc_fence_after();
       if (elect_lane()) {
         for (int m = 0; m < MT; ++m) {
@@ -721,6 +772,7 @@ __global__ void __launch_bounds__(kAqThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == kAqWorkers) {
+    if (lds32(gave_up) != 0u) aq_drain(bar_d, bar_q, 0, p);
     tc_fence_after();
     tmem_dealloc(tmem, kCols);
   }
@@ -765,7 +817,8 @@ __global__ void __launch_bounds__(kAmThreads, 1)
   float* lse_s = reinterpret_cast<float*>(smem + L_::lse_off(D));
   float* part_s = reinterpret_cast<float*>(smem + L_::part_off(D));
   float* sum_s = reinterpret_cast<float*>(smem + L_::sum_off(D));
-  const uint32_t full0 = sbase + L_::bar_off(D), bar_q = full0 + 32u, bar_s = bar_q + 8u, bar_x = bar_s + 8u;
+  const uint32_t full0 = sbase + L_::bar_off(D), bar_q = full0 + 32u, bar_s = bar_q + 8u, bar_x = bar_s + 8u, bar_d = bar_x + 8u;
+  const uint32_t gave_up = full0 + 8u * 8u + 4u;  // behind the address of tensor memory
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L_::slot_off(D));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = p.C, rank = blockIdx.x % C;
@@ -776,10 +829,12 @@ __global__ void __launch_bounds__(kAmThreads, 1)
   constexpr uint32_t kCols = N < 32 ? 32 : N;
 
   if (tid == 0) {
-    for (int i = 0; i < MT; ++i) mbar_init(full0 + 8u * i, kAmWorkers);
+    for (int i = 0; i < MT; ++i) mbar_init(full0 + 8u * i, kAmWorkers + (p.fault != 0 && blockIdx.x == 0 ? 1u : 0u));
     mbar_init(bar_q, 1);
     mbar_init(bar_s, 1);
     mbar_init(bar_x, kAmWorkers);  // queries reordered
+    mbar_init(bar_d, 1);           // the end of a CTA that gave up
+    tmem_slot[1] = 0u;             // gave_up
     fence_mbar_init();
   }
   if (warp == kAmWorkers) {
@@ -801,14 +856,14 @@ __global__ void __launch_bounds__(kAmThreads, 1)
   r_load = aq_checked(p, false, r_load);
   r = aq_checked(p, false, r);
   float total = 0.0f;
-  int turn = 0;
+  int turn = 0, loads = 0;  // tiles, and the copies of queries that were issued for them
   for (int t = rank, g_held = -1; t < tiles; t += C, ++turn) {
     const int g = t / p.HT, ht = t % p.HT, heads = min(N, G - ht * N);
     if (warp < kAmWorkers) {
       float fac = r >= 0 ? p.scale_log2 : 0.0f;  // (the scale's load is on its way while the rows are)
       if (FMT != kFmtBf16 && r >= 0) fac *= aq_scale<FMT>(p, b, r, g);
       auto swap_queries = [&]() {
-        aq_wait(bar_q, (uint32_t)(turn & 1), p);
+        aq_wait<false>(bar_q, (uint32_t)(turn & 1), p, gave_up);
         aq_swap_queries(q_s, DB * N * 128, tid, kAmWorkers * 32);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_x);
@@ -843,7 +898,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
         lse_s[tid] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
       }
       named_bar_sync(1, kAmWorkers * 32);
-      aq_wait(bar_s, (uint32_t)(turn & 1), p);
+      aq_wait<false>(bar_s, (uint32_t)(turn & 1), p, gave_up);
       tc_fence_after();
       float z[NH];
       aq_tmem_ld<NH>(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(part * NH), z);
@@ -859,16 +914,21 @@ __global__ void __launch_bounds__(kAmThreads, 1)
       tc_fence_before();
       named_bar_sync(1, kAmWorkers * 32);  // lse_s and the scores have been read
     } else {
-      if (elect_lane()) {
-        // (the scores of the tile before have been read: the workers' barrier above precedes their arrivals)
-        mbar_arrive_expect_tx(bar_q, (uint32_t)(DB * N * 128));
-        tma_load_3d(q_s, &tm_q, 0, b * p.H + g * G + ht * N, 0, bar_q);
+      // (the scores of the tile before have been read: the workers' barrier above precedes
+      // their arrivals.  After a wait that ran out the copy before may not have landed, and
+      // bar_q would get a second arrival in its phase)
+      if (turn == 0 || __all_sync(0xffffffffu, lds32(gave_up) == 0u)) {
+        if (elect_lane()) {
+          mbar_arrive_expect_tx(bar_q, (uint32_t)(DB * N * 128));
+          tma_load_3d(q_s, &tm_q, 0, b * p.H + g * G + ht * N, 0, bar_q);
+        }
+        ++loads;
       }
-      aq_wait(bar_x, (uint32_t)(turn & 1), p);
+      aq_wait<false>(bar_x, (uint32_t)(turn & 1), p, gave_up);
       constexpr uint32_t id = idesc_bf16_f32(kAqRows, N);
       const uint64_t ka = sw128_kmajor_desc(rows_s), kb = sw128_kmajor_desc(q_s);
       for (int m = 0; m < MT; ++m) {
-        aq_wait(full0 + 8u * (uint32_t)m, (uint32_t)(turn & 1), p);
+        aq_wait<false>(full0 + 8u * (uint32_t)m, (uint32_t)(turn & 1), p, gave_up);
         tc_fence_after();
         if (elect_lane()) {
           const uint64_t a0 = desc_at(ka, (uint32_t)m * 2 * kAqBlock), b0 = desc_at(kb, (uint32_t)m * 2 * N * 128);
@@ -881,7 +941,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
         }
         __syncwarp();
       }
-      aq_wait(bar_s, (uint32_t)(turn & 1), p);  // the queries' memory is free
+      aq_wait<false>(bar_s, (uint32_t)(turn & 1), p, gave_up);  // the queries' memory is free
     }
     g_held = g;
   }
@@ -894,7 +954,8 @@ __global__ void __launch_bounds__(kAmThreads, 1)
   __syncwarp();
   if (C > 1) cluster_wait();
   if (tid < kAqRows) {
-    const float s = (part_s[tid] + part_s[kAqRows + tid]) + (part_s[2 * kAqRows + tid] + part_s[3 * kAqRows + tid]);
+    float s = (part_s[tid] + part_s[kAqRows + tid]) + (part_s[2 * kAqRows + tid] + part_s[3 * kAqRows + tid]);
+    if (lds32(gave_up) != 0u) s = 0.0f;  // not counted, rather than counted wrong
     if (C == 1)
       sum_s[tid] = s;
     else
@@ -911,6 +972,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == kAmWorkers) {
+    if (lds32(gave_up) != 0u) aq_drain(bar_d, bar_q, (uint32_t)((loads - 1) & 1), p);
     tc_fence_after();
     tmem_dealloc(tmem, kCols);
   }

@@ -263,6 +263,7 @@ extern "C" int ds_sparse_attention_q8(const void* q, const void* codes, int64_t 
   p.lse = lse;
   p.status = s->status;
   p.wait_ns = wait_limit();
+  p.fault = take_planted_fault();
   p.cache_bstride = codes_batch_stride * kv_heads * d;
   p.scales_bstride = scales_batch_stride * kv_heads;
   p.T = T;
@@ -339,6 +340,7 @@ extern "C" int ds_attention_mass(const void* q, const void* cache, int64_t cache
   p.mass = mass;
   p.status = s->status;
   p.wait_ns = wait_limit();
+  p.fault = take_planted_fault();
   p.cache_bstride = cache_batch_stride * kv_heads * d;
   p.scales_bstride = scales_batch_stride * kv_heads;
   p.mass_bstride = mass_batch_stride;
