@@ -138,7 +138,8 @@ __device__ __forceinline__ void ce_keys(const CeParams& p, const float* mass, ui
 
 __global__ void __launch_bounds__(kCeThreads) cache_evict_kernel(const CeParams p) {
   extern __shared__ uint32_t keys[];                // [min(share, kCeKeys)]
-  __shared__ uint32_t hist[2][kCeBins];             // a digit's counts; two, so that one barrier parts two digits
+  // a digit's counts; two, so that one barrier parts two digits; read in pairs
+  __shared__ alignas(8) uint32_t hist[2][kCeBins];
   __shared__ uint32_t warp_s[2][32];
   __shared__ uint32_t found[3];                     // digit of the last key, blocks to take of it, blocks that have it
   __shared__ uint2 counts;                          // this CTA's blocks above the key, and equal to it
