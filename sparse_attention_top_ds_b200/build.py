@@ -79,13 +79,9 @@ def front_command(out):
 def build(force=False, verbose=False):
     """Compile csrc/lib.cu into libdstopk.so and libdstopk_debug.so and
     csrc/front.cpp into _front.so next to this file (all side by side); return
-    the release library's path."""
-    jobs = []
-    if force or front_stale():
-        cmd = front_command(FRONT + ".tmp")
-        if verbose:
-            print(" ".join(cmd), file=sys.stderr)
-        jobs.append((FRONT, FRONT + ".tmp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
+    the release library's path.  Without PyTorch the C libraries are all there is to
+    build: _front.so serves its tensors only."""
+    jobs, errors = [], []
     for lib, extra in ((LIB, []), (LIB_DEBUG, ["-DDS_DEBUG"])):
         if not force and not stale(lib):
             continue
@@ -95,7 +91,18 @@ def build(force=False, verbose=False):
             print(" ".join(cmd), file=sys.stderr)
         proc = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
         jobs.append((lib, tmp, proc))
-    errors = []
+    if force or front_stale():
+        tmp = FRONT + ".tmp"
+        try:
+            cmd = front_command(tmp)
+        except ImportError as e:
+            print(f"_front.so is not built: {e}", file=sys.stderr)
+        except (RuntimeError, OSError) as e:
+            errors.append(str(e))
+        else:
+            if verbose:
+                print(" ".join(cmd), file=sys.stderr)
+            jobs.append((FRONT, tmp, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
     for lib, tmp, proc in jobs:
         out, err = proc.communicate()
         if proc.returncode != 0:
