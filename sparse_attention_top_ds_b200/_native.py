@@ -498,6 +498,11 @@ def _load_front():
     global _front
     import torch  # noqa: F401  (loads the libraries that the extension is linked to)
     lib = load()
+    from . import build
+    made = build.front_built_for()
+    if made not in (None, build.front_tag()):  # loading it could end the process
+        raise RuntimeError(f"_front.so was built for {made}, not for {build.front_tag()}; build it with "
+                           "`python -m sparse_attention_top_ds_b200.build`")
     try:
         from . import _front as front
     except ImportError as e:

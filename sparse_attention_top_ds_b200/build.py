@@ -53,8 +53,29 @@ def stale(lib=LIB):
     return any(os.path.getmtime(f) > t for f in sources())
 
 
+def front_tag():
+    """What _front.so is compiled for: this Python and this torch (ImportError without one)."""
+    import importlib.metadata
+    import sysconfig
+    try:
+        version = importlib.metadata.version("torch")  # without the seconds that importing it takes
+    except importlib.metadata.PackageNotFoundError:
+        import torch
+        version = torch.__version__
+    return f"{sysconfig.get_config_var('SOABI')}, torch {version}"
+
+
+def front_built_for():
+    """The front_tag that _front.so was compiled with, or None."""
+    try:
+        with open(FRONT + ".tag") as f:
+            return f.read()
+    except OSError:
+        return None
+
+
 def front_stale():
-    if not os.path.exists(FRONT):
+    if not os.path.exists(FRONT) or front_built_for() != front_tag():
         return True
     t = os.path.getmtime(FRONT)
     return any(os.path.getmtime(f) > t for f in (HEADER, FRONT_SOURCE))
@@ -91,24 +112,28 @@ def build(force=False, verbose=False):
             print(" ".join(cmd), file=sys.stderr)
         proc = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
         jobs.append((lib, tmp, proc))
-    if force or front_stale():
-        tmp = FRONT + ".tmp"
-        try:
+    tmp = FRONT + ".tmp"
+    cmd = None
+    try:
+        if force or front_stale():
             cmd = front_command(tmp)
-        except ImportError as e:
-            print(f"_front.so is not built: {e}", file=sys.stderr)
-        except (RuntimeError, OSError) as e:
-            errors.append(str(e))
-        else:
-            if verbose:
-                print(" ".join(cmd), file=sys.stderr)
-            jobs.append((FRONT, tmp, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
+    except ImportError as e:
+        print(f"_front.so is not built: {e}", file=sys.stderr)
+    except (RuntimeError, OSError) as e:
+        errors.append(str(e))
+    if cmd:
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        jobs.append((FRONT, tmp, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
     for lib, tmp, proc in jobs:
         out, err = proc.communicate()
         if proc.returncode != 0:
             errors.append(f"the compiler failed for {os.path.basename(lib)}:\n" + out + err)
         else:
             os.replace(tmp, lib)
+            if lib == FRONT:
+                with open(FRONT + ".tag", "w") as f:
+                    f.write(front_tag())
     if errors:
         raise RuntimeError("\n".join(errors))
     return LIB

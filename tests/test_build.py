@@ -53,3 +53,24 @@ def test_the_c_libraries_are_built_where_the_extension_cannot_be(compiled, monke
     with pytest.raises(RuntimeError, match="g\\+\\+ not found"):
         build.build()
     assert sorted(compiled) == LIBS
+
+
+def test_an_extension_for_another_torch_is_built_again(compiled, monkeypatch):
+    build.build()
+    assert not build.front_stale()
+    here = build.front_tag()
+    monkeypatch.setattr(build, "front_tag", lambda: here + "1")
+    assert build.front_stale()
+    build.build()
+    assert compiled.count("_front.so") == 2 and not build.front_stale()
+
+
+def test_an_extension_for_another_torch_is_not_loaded(compiled, monkeypatch):
+    from sparse_attention_top_ds_b200 import _native
+    build.build()
+    with open(build.FRONT + ".tag", "w") as f:
+        f.write("cpython-999, torch 0.1")
+    monkeypatch.setattr(_native, "_front", None)
+    monkeypatch.setattr(_native, "load", lambda: None)
+    with pytest.raises(RuntimeError, match="built for cpython-999, torch 0.1, not for .*build it with"):
+        _native._load_front()
