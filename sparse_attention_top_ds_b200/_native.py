@@ -656,7 +656,8 @@ def _cache8(codes, scales, block, batch, dev):
 def ds_cache_quantize(rows, codes, scales, block, pos=None, length=None, stream=None):
     """Write bfloat16 rows into an 8-bit cache, in place.
 
-    rows    bf16 [batch, n, kv_heads, d] (any batch and row strides);
+    rows    bf16 [batch, n, kv_heads, d], 16-byte aligned; its batch stride (0 too) and its row
+            stride (kv_heads * d or more) are multiples of 8 elements;
     codes   float8_e4m3fn or int8 [batch, T, kv_heads, d];
     scales  float32 [batch, ceil(T / block), kv_heads];
     block   rows that share a scale: 1, 2, 4 .. 128;
@@ -675,6 +676,9 @@ def ds_cache_quantize(rows, codes, scales, block, pos=None, length=None, stream=
     if ch != kv_heads or cd != d or codes.dim() != 4:
         raise ValueError("codes must be [batch, T, kv_heads, d] with the rows' kv_heads and d")
     x = _rows_arg(rows, torch.bfloat16, rows.shape, dev, "rows", 2)
+    if (batch > 1 and rows.stride(0) % 8) or (n > 1 and (rows.stride(1) % 8 or rows.stride(1) < kv_heads * d)):
+        raise ValueError("rows: the batch and row strides must be multiples of 8 elements, the row stride at least "
+                         f"kv_heads * d, got strides {list(rows.stride())}")
     args = (x, rows.stride(0) if batch > 1 else 0, rows.stride(1) if n > 1 else kv_heads * d, batch, n, kv_heads, d, dt, block,
             _opt(pos, torch.int32, (batch,), dev, "pos"), _opt(length, torch.int32, (batch,), dev, "length"), c, cstep, s,
             sstep, T)

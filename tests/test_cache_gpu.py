@@ -820,6 +820,19 @@ def test_front_end_refusals(cuda_device):
     ok_status()
 
 
+def test_quantize_says_which_strides_it_takes(cuda_device):
+    codes, scales = torch.zeros(2, 8, 1, 64, dtype=torch.int8, device="cuda"), torch.zeros(2, 2, 1, device="cuda")
+    wide = torch.zeros(2, 8, 1, 100, dtype=torch.bfloat16, device="cuda")
+    odd = torch.zeros(2 * 600, dtype=torch.bfloat16, device="cuda").as_strided((2, 8, 1, 64), (516, 64, 64, 1))
+    for rows in (wide[..., :64],                                            # a row stride of 100
+                 odd,                                                       # a batch stride of 516
+                 wide[:, :1, :, :64].expand(2, 8, 1, 64),                   # one row eight times
+                 torch.zeros(900, dtype=torch.bfloat16, device="cuda").as_strided((2, 8, 1, 64), (512, 32, 64, 1))):
+        with pytest.raises(ValueError, match="strides must be multiples of 8"):
+            ds.ds_cache_quantize(rows, codes, scales, 4)
+    ok_status()
+
+
 # ---------------------------------------------------------------- together, as they would be used
 
 def serve(q, rows, win, sink, block, budget, fmt, steps):
