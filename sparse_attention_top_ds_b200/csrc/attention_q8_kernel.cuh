@@ -189,8 +189,8 @@ __device__ __forceinline__ void aq_store(const uint4 (&v)[4 * K], int m, int n, 
         decode8x4<FMT>(x.y, lo.z, lo.w, top);
         decode8x4<FMT>(x.z, hi.x, hi.y, top);
         decode8x4<FMT>(x.w, hi.z, hi.w, top);
-        // one NaN makes the row's scores NaN, wherever it is.  (The check takes 560 us to
-        // 587 at 512 tokens over 2048 rows, and 19.1 to 19.5 in the decode call.)
+        // one NaN makes the row's scores NaN, wherever it is.  (The check took 512 tokens
+        // over 2048 rows from 560 us to 587, and the decode call from 19.1 to 19.5.)
         if (FMT == kFmtE4m3 && e4m3_nan(top)) lo.x = 0x7fc07fc0u;
       }
       const uint32_t at = at0 + (uint32_t)(e * kAqBlock + k * 64 * 128);
@@ -227,8 +227,8 @@ __device__ __forceinline__ void aq_swap_queries(uint32_t q, int bytes, int threa
 // up to 1.7 times as far from the exact ones as their own rounding puts them.  With 64
 // heads the second half would not fit tensor memory (576 columns).  A call of at most 64
 // rows leaves half of P^T's 128 rows free: they take the rests, with MMAs of their own.
-// More rows average the roundings out (585 us at 512 tokens over 2048 rows, 1.3 times the
-// distance; such MMAs would add a fifth to a chunk): their weights are rounded once.
+// More rows average the roundings out (512 tokens over 2048 rows: 1.3 times the distance),
+// and such MMAs would add a fifth to a chunk's time: their weights are rounded once.
 //
 // A chunk passes through in turn: the widened rows serve both products, so
 // nothing of the next chunk can be stored before the weighted sum has freed its
@@ -249,8 +249,8 @@ __device__ __forceinline__ void aq_swap_queries(uint32_t q, int bytes, int threa
 // channels x 4 heads of its O^T to the CTA that owns them, and each owner adds
 // the C contributions in rank order, scaled to the common maximum.
 //
-// 128 heads of 512 channels: 8 batch rows over 1024 + 128 rows take 19.6 us, 512 over
-// 2048 rows of one cache 585 us (28% of the measured tensor rate).  What bounds it is
+// 128 heads of 512 channels: 8 batch rows over 1024 + 128 rows take 19.2 us, 512 over
+// 2048 rows of one cache 594 us (28% of the measured tensor rate).  What bounds it is
 // the chain within a chunk, and shared memory: the MMAs and the widened rows want half
 // of a chunk's time of its bandwidth.
 constexpr int kAqWorkers = 8;
@@ -788,7 +788,9 @@ __global__ void __launch_bounds__(kAqThreads, 1)
 // With a row to a thread the sum over heads never leaves the thread: four
 // threads share a row, their sums and then the CTAs' are added in a fixed order,
 // and each slot's total is added to its account once.  8 batch rows of 128 heads of 512
-// channels over 1024 rows take 7.7 us, a floor of 0.8: the chain slots, rows, scores.
+// channels over 1024 rows take 7.4 us, a floor of 0.8: the chain slots, rows, scores.
+// 512 of them over 2048 rows of one cache take 836 us, a floor of 83: a CTA takes one
+// chunk, and nothing of the next is on its way meanwhile.
 constexpr int kAmWorkers = 16;
 constexpr int kAmThreads = (kAmWorkers + 1) * 32;
 constexpr int kAmMaxCluster = 8;

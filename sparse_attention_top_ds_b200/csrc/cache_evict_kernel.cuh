@@ -43,8 +43,12 @@ __device__ __forceinline__ int ce_len(const int32_t* len, int T, int b, int* sta
 // counts its share, reads the counts of the others and finds the digit by itself,
 // so a digit costs one cluster barrier.  Then each CTA knows how many blocks stay
 // before its share, each thread how many before its own run of blocks, and the
-// list comes out in order.  The bytes (4 per row) are few: what bounds it is the
-// chain of barriers (4096 rows one by one 8.7 us, 8 x 32768 in blocks of 64 9.3).
+// list comes out in order.  The bytes (4 per row) are few: what bounds it is a chain
+// of short steps, each a pass over the CTA's keys or bins between two barriers, at 0.4
+// instructions per scheduler and cycle.  4096 rows one by one, in one CTA, take 8.1 us:
+// of 7.8 within the kernel, the length 0.8, the keys 1.8, two digits (counted 0.6, found
+// 0.8, counted and found 1.7), counting what stays 0.9, the list 1.1.  8 x 32768 in blocks of 64 take 9.5, with a cluster's barriers and reads
+// (keys 2.0, digits 0.8, 1.3 and 2.2, list 1.6).
 constexpr int kCeThreads = 1024;
 constexpr int kCeMaxCluster = 8;
 constexpr int kCeBins = 2048;

@@ -280,9 +280,13 @@ extern "C" int ds_sparse_attention_q8(const void* q, const void* codes, int64_t 
   // 4.4 us with 16, 32 and 64 heads (the MMAs cost the same up to 64), the parts of a
   // call beside its turns 5.5, 5.5 and 8.5 us, and 7.1, 8.1 and 12.9 where a cluster
   // exchanges partial results; what has the least of both, over all waves of CTAs, is
-  // taken.  128 heads over 1024 + 128 rows: one batch row 16 heads, 9 CTAs 10.3 us
-  // (64, 10: 17), eight 32, 4 18.4 us (64, 6: 21.5), thirty-two 64, 2 35.0 us (32, 1:
-  // 37.3).  (Before e4m3 codes were checked for NaN, which takes 2 to 5% more.)
+  // taken.  128 heads over 1024 + 128 rows: one batch row 16 heads, 9 CTAs 9.7 us,
+  // eight 32, 3 18.9 us, sixty-four 64, 1 63 us.  The figures are those of 512 channels
+  // before e4m3 codes were checked for NaN (2 to 5% more), but what they choose is right
+  // elsewhere too: of all heads and CTAs, each forced, on 40 shapes (64, 128, 192, 256 and
+  // 512 channels; 1 to 300 batch rows; 8 to 128 heads to a KV head) none was more than 1%
+  // faster, but for 16 batch rows of 128 heads, where 64, 3 takes 7 to 9% less than
+  // the 32, 2 chosen at 64 to 256 channels, and 2% less at 512.
   const int G = heads / kv_heads;
   auto turns = [&](int r, int c) { return ((k + r - 1) / r + (W + r - 1) / r + c - 1) / c; };
   int n = 0;
@@ -401,8 +405,9 @@ extern "C" int ds_cache_evict(const float* mass, int64_t mass_batch_stride, int 
   p.first = keep_first;
   p.last = keep_last;
   // CTAs of a batch row: a share of some 8192 rows to each.  8 rows of 32768 in blocks
-  // of 64 took 10.3 us with 4 CTAs each, 11.1 with 2 and 13.1 with 8 (every CTA reads
-  // the others' counts); in blocks of 1 16.7, 27.7 and 16.3.
+  // of 64 take 9.3 us with 4 CTAs each, 9.9 with 2 and 12.1 with 8 (every CTA reads the
+  // others' counts); in blocks of 1 15.3, 24.9 and 15.2.  4096 rows take 8.4 us with 1, 8.7
+  // with 2.
   int C = 1;
   while (C < kCeMaxCluster && T / C > 8192) C *= 2;
   const int nb = (T + block - 1) / block;

@@ -63,7 +63,8 @@ __device__ __forceinline__ uint2 cq_encode8(const uint4& x, float inv) {
 // a magnitude order like its value).  NT is the smallest that holds the block.
 // Bytes bound it, 2 read and 1 written for each value, but only just: a value costs
 // about 5 instructions, so addresses are advanced, not worked out, per piece (8 x 16384
-// rows of 512 in blocks of 64: 37.9 us, 5.3 TB/s, 81% of the copy rate; worked out, 52).
+// rows of 512 in blocks of 64: 37.8 us in graph replays, 38.7 call by call, 5.2 to 5.3
+// TB/s, 79 to 81% of the copy rate; worked out, 52).
 constexpr int kCqPieces = 8;
 
 template <int FMT, int NT>
